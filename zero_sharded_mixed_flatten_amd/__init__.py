@@ -1,7 +1,8 @@
 """zero_sharded_mixed_flatten_amd -- one data-parallel rank's sharded,
 mixed-precision optimizer step on MI355X (gfx950).
 
-A thin ctypes binding over libzero_shard.so (include/zero_shard.h).  Every
+A thin ctypes binding over libzero_shard.so (include/zero_shard.h; the layer
+products of include/zero_linear.h in _linear.py).  Every
 function here has the name of the C entry point it calls and only marshals
 arguments: torch tensors become device pointers and dtype codes, the current
 torch stream becomes the HIP stream.  All work runs in the library's HIP
@@ -834,9 +835,18 @@ def library_path() -> str:
     return LIB_PATH
 
 
+from ._linear import (  # noqa: E402  (the second header's part of the binding)
+    ZERO_ACT_GELU, ZERO_ACT_GELU_TANH, ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_SILU, ZERO_LINEAR,
+    ZERO_LINEAR_DGRAD, ZERO_LINEAR_WGRAD, ZeroDropout, zero_dropout, zero_linear,
+    zero_linear_dgrad, zero_linear_wgrad, zero_linear_workspace_bytes)
+
 __all__ = ["zero_flatten_layout", "zero_shard_segments", "zero_dim0_layout", "zero_dim0_segments", "zero_shard_reduce",
            "zero_shard_adamw", "zero_shard_adamw_ex", "zero_loss_scale_update",
            "new_loss_scale", "read_loss_scale", "zero_shard_step", "zero_flat_gather",
            "zero_flat_scatter", "zero_reshard", "zero_q8_quantize", "zero_q8_dequantize",
            "zero_shard_step_q8", "zero_sumsq_workspace_bytes", "q8_blocks", "ZERO_Q8_BLOCK", "zero_model_state_bytes", "zero_comm_bytes",
-           "zero_adam_step", "AdamWHParams", "ZeroLayout", "ZeroError", "ZeroValueError", "ZERO_BF16", "ZERO_FP16", "ZERO_FP32", "library_path"]
+           "zero_adam_step", "AdamWHParams", "ZeroLayout", "ZeroError", "ZeroValueError", "ZERO_BF16", "ZERO_FP16", "ZERO_FP32", "library_path",
+           "zero_linear", "zero_linear_dgrad", "zero_linear_wgrad", "zero_dropout",
+           "zero_linear_workspace_bytes", "ZeroDropout", "ZERO_LINEAR", "ZERO_LINEAR_DGRAD",
+           "ZERO_LINEAR_WGRAD", "ZERO_ACT_NONE", "ZERO_ACT_RELU", "ZERO_ACT_GELU",
+           "ZERO_ACT_GELU_TANH", "ZERO_ACT_SILU"]

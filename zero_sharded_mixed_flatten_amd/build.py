@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libzero_shard.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("zero_shard.hip", "quant8.hip", "flat_copy.hip", "layout.cpp")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("zero_shard.hip", "quant8.hip", "flat_copy.hip",
+                                                   "linear.hip", "dropout.hip", "layout.cpp")]
 
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -24,7 +25,8 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
 
 def build(verbose: bool = False) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
-    # only the entry points of include/zero_shard.h are exported
+    # only the entry points of include/zero_shard.h and include/zero_linear.h
+    # are exported
     cmd = [HIPCC] + FLAGS + ["-I", os.path.join(ROOT, "include"),
                              "-o", LIB + ".tmp"] + SOURCES
     if verbose:

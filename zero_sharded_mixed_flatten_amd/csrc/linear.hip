@@ -1,0 +1,612 @@
+// linear.hip -- gfx950 kernels of the layer products on the flat buffers:
+// zero_linear, zero_linear_dgrad, zero_linear_wgrad.
+//
+// All three are one contraction, out[i][j] = sum over c of P(i, c) Q(j, c),
+// over operands stored with c contiguous ("rows of c") or with i or j
+// contiguous ("rows of lanes"):
+//   linear  i = m, j = n, c = k:  P = x  (rows of c),     Q = W (rows of c)
+//   dgrad   i = m, j = k, c = n:  P = dy (rows of c),     Q = W (rows of lanes)
+//   wgrad   i = n, j = k, c = m:  P = dy (rows of lanes), Q = x (rows of lanes)
+//
+// A workgroup computes a BI x BJ tile with v_mfma_f32_16x16x32.  Q is the
+// instruction's row operand, so that a lane ends up with four consecutive j
+// of one i: its outputs, residuals and biases are vectors.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "linear_common.h"
+
+namespace {
+
+using namespace zero_host;
+using namespace zero_linear_impl;
+
+using s16x4 = short __attribute__((ext_vector_type(4)));
+using s16x8 = short __attribute__((ext_vector_type(8)));
+
+constexpr int kBK = 64;  // contraction elements of one step
+
+enum Op { FWD = ZERO_LINEAR, DGRAD = ZERO_LINEAR_DGRAD, WGRAD = ZERO_LINEAR_WGRAD };
+
+struct Epilogue {
+    const uint16_t *bias;
+    const void *res;
+    void *out;
+    uint16_t *z;      // linear: written; dgrad: read
+    void *db;         // wgrad
+    int64_t ldr, ldo, ldz;
+    int32_t act, out_f32, accumulate;
+    int32_t vec;      // every row of out, res, z and bias is aligned for four elements
+    Drop drop;
+};
+
+struct Args {
+    const uint16_t *p, *q;
+    int64_t ldp, ldq;
+    int64_t ni, nj, nc;
+    int64_t chunk;    // contraction elements of a part, a multiple of kBK
+    int32_t parts;
+    int32_t tiles_i, tiles_j;
+    float *partial;   // [parts][ni][njp], then the column sums [parts][ni]
+    Epilogue e;
+};
+
+__host__ __device__ inline int64_t padded4(int64_t n) { return (n + 3) & ~int64_t(3); }
+
+// ---------------------------------------------------------------------------
+// matrix instructions
+
+template <class T>
+__device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c);
+template <>
+__device__ __forceinline__ f32x4 mfma<BF16>(s16x8 a, s16x8 b, f32x4 c) {
+    using v = __bf16 __attribute__((ext_vector_type(8)));
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v, a),
+                                                   __builtin_bit_cast(v, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x4 mfma<FP16>(s16x8 a, s16x8 b, f32x4 c) {
+    using v = _Float16 __attribute__((ext_vector_type(8)));
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v, a),
+                                                  __builtin_bit_cast(v, b), c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// epilogue of four neighbouring outputs (i, j..j+3), n of them inside
+
+template <int OP, class T>
+__device__ __forceinline__ void emit(const Epilogue &e, int64_t i, int64_t j, int n, f32x4 v,
+                                     u32x4 words, int half) {
+    const bool vec = e.vec != 0;
+    if constexpr (OP == WGRAD) {
+        if (e.out_f32) {
+            float *o = static_cast<float *>(e.out) + i * e.ldo + j;
+            if (e.accumulate) v = load32(o, n, vec) + v;
+            store32(o, v, n, vec);
+        } else {
+            uint16_t *o = static_cast<uint16_t *>(e.out) + i * e.ldo + j;
+            if (e.accumulate) v = load16<T>(o, n, vec) + v;
+            store16<T>(o, v, n, vec);
+        }
+        return;
+    }
+    if constexpr (OP == FWD) {
+        if (e.bias != nullptr) v += load16<T>(e.bias + j, n, vec);
+        if (e.z != nullptr) store16<T>(e.z + i * e.ldz + j, v, n, vec);
+        if (e.act != ZERO_ACT_NONE) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = act_value(v[k], e.act);
+        }
+    } else if (e.act != ZERO_ACT_NONE) {
+        const f32x4 z = load16<T>(e.z + i * e.ldz + j, n, vec);
+        if (e.act == ZERO_ACT_RELU) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = z[k] > 0.0f ? v[k] : 0.0f;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] *= act_slope(z[k], e.act);
+        }
+    }
+    if (e.drop.on) v = drop_apply(e.drop, words, half, v);
+    if (e.out_f32) {
+        if (e.res != nullptr)
+            v = load32(static_cast<const float *>(e.res) + i * e.ldr + j, n, vec) + v;
+        store32(static_cast<float *>(e.out) + i * e.ldo + j, v, n, vec);
+    } else {
+        if (e.res != nullptr)
+            v = load16<T>(static_cast<const uint16_t *>(e.res) + i * e.ldr + j, n, vec) + v;
+        store16<T>(static_cast<uint16_t *>(e.out) + i * e.ldo + j, v, n, vec);
+    }
+}
+
+// the quads at j and j + 16 (j a multiple of 4 in the first half of its group
+// of 32 columns), which share one draw of the mask
+template <int OP, class T>
+__device__ __forceinline__ void emit_pair(const Epilogue &e, int64_t i, int64_t j, int64_t nj,
+                                          uint64_t stream, f32x4 v0, f32x4 v1) {
+    if (j >= nj) return;
+    u32x4 words = {0u, 0u, 0u, 0u};
+    if (OP != WGRAD && e.drop.on)
+        words = drop_words(e.drop, stream, static_cast<uint32_t>(i),
+                           static_cast<uint32_t>((j >> 5) * 4 + ((j & 15) >> 2)));
+    emit<OP, T>(e, i, j, static_cast<int>(nj - j < 4 ? nj - j : 4), v0, words, 0);
+    const int64_t j1 = j + 16;
+    if (j1 < nj) emit<OP, T>(e, i, j1, static_cast<int>(nj - j1 < 4 ? nj - j1 : 4), v1, words, 1);
+}
+
+template <class T>
+__device__ __forceinline__ void emit_db(const Epilogue &e, int64_t i, float v) {
+    if (e.out_f32) {
+        float *o = static_cast<float *>(e.db) + i;
+        *o = e.accumulate ? *o + v : v;
+    } else {
+        uint16_t *o = static_cast<uint16_t *>(e.db) + i;
+        *o = T::down(e.accumulate ? T::up(*o) + v : v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// tiles in shared memory, in 16-byte pieces of eight elements
+//
+// Rows of c: [ROWS][64], piece (row, s) at row * 8 + (s ^ (row & 7)); a
+// lane's operand is one piece, eight consecutive c of its row.  The exclusive
+// or spreads the pieces that eight lanes read at once over all banks.
+//
+// Rows of lanes: [64][ROWS], piece (c, s) at c * ROWS / 8 + (s ^ 2 (c & M)),
+// M = 7 (3 for 64 lanes): 32-byte units of 16 lanes stay whole and those of
+// neighbouring c fall into different banks.  ds_read_b64_tr_b16 reads four
+// rows of such a unit and hands every lane the four c of its own column: two
+// of them make an operand.
+
+template <int ROWS>
+constexpr int kSwizzle = ROWS >= 128 ? 7 : 3;
+
+template <bool KC, int ROWS>
+__device__ __forceinline__ int piece_row(int pos) {
+    return KC ? pos >> 3 : pos / (ROWS / 8);
+}
+template <bool KC, int ROWS>
+__device__ __forceinline__ int piece_slot(int pos) {
+    if (KC) return (pos & 7) ^ ((pos >> 3) & 7);
+    return (pos % (ROWS / 8)) ^ (2 * ((pos / (ROWS / 8)) & kSwizzle<ROWS>));
+}
+
+// A piece of the operand as eight elements, zeros past the row's or the
+// contraction's end: one unaligned 16-byte load where all eight exist (global
+// memory takes any alignment), element loads at the ends.
+__device__ __forceinline__ u32x4 load_piece(const uint16_t *p, int64_t n) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (n >= 8) {
+        __builtin_memcpy(&v, p, 16);
+    } else if (n > 0) {
+        uint16_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = e < n ? p[e] : 0;
+        __builtin_memcpy(&v, h, 16);
+    }
+    return v;
+}
+
+template <bool KC, int ROWS, int THREADS>
+struct Stage {
+    static constexpr int N = ROWS * kBK / 8 / THREADS;
+    u32x4 v[N];
+    // rows [r0, rows), contraction [c0, c1)
+    __device__ __forceinline__ void load(const uint16_t *p, int64_t ld, int64_t r0, int64_t rows,
+                                         int64_t c0, int64_t c1) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int pos = n * THREADS + static_cast<int>(threadIdx.x);
+            const int row = piece_row<KC, ROWS>(pos), s = piece_slot<KC, ROWS>(pos);
+            if (KC) {
+                const int64_t r = r0 + row, c = c0 + s * 8;
+                v[n] = load_piece(p + r * ld + c, r < rows ? c1 - c : 0);
+            } else {
+                const int64_t c = c0 + row, r = r0 + s * 8;
+                v[n] = load_piece(p + c * ld + r, c < c1 ? rows - r : 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t *tile) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            *reinterpret_cast<u32x4 *>(tile + (n * THREADS + static_cast<int>(threadIdx.x)) * 8) =
+                v[n];
+    }
+};
+
+// a lane's operand of a 16-row block: eight consecutive c from kk * 32 on
+template <bool KC, int ROWS>
+__device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int kk, int lane) {
+    if constexpr (KC) {
+        const int r = lane & 15, s = kk * 4 + (lane >> 4);
+        return *reinterpret_cast<const s16x8 *>(tile + (row0 + r) * kBK + ((s ^ (r & 7)) * 8));
+    } else {
+        const int t = lane & 15, g = lane >> 4;
+        using lds4 = __attribute__((address_space(3))) s16x4;
+        s16x8 f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = kk * 32 + g * 8 + h * 4 + (t >> 2);
+            const int unit = (row0 >> 4) ^ (c & kSwizzle<ROWS>);
+            const uint16_t *a = tile + c * ROWS + unit * 16 + (t & 3) * 4;
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(a));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[h * 4 + e] = x[e];
+        }
+        return f;
+    }
+}
+
+// The tile of this workgroup.  Workgroups go round the 8 XCDs in turn; each
+// XCD is given one contiguous run of tiles, taken in bands of 8 rows of
+// tiles, so that the tiles at work in one L2 share their operands.
+__device__ __forceinline__ void tile_of(const Args &a, int &ti, int &tj) {
+    const int total = a.tiles_i * a.tiles_j, b = static_cast<int>(blockIdx.x);
+    const int x = b & 7, q = total >> 3, r = total & 7;
+    const int id = x * q + (x < r ? x : r) + (b >> 3);
+    const int band = 8 * a.tiles_j, first = id / band * 8;
+    const int high = min(8, a.tiles_i - first), in = id - first * a.tiles_j;
+    ti = first + in % high;
+    tj = in / high;
+}
+
+template <int OP, class T, int BI, int BJ, int WI, int WJ>
+__global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
+    constexpr bool PKC = OP != WGRAD, QKC = OP == FWD;
+    constexpr int THREADS = WI * WJ * kWave;
+    constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
+    static_assert(FJ % 2 == 0, "mask draws pair two 16-column blocks");
+    __shared__ __attribute__((aligned(1024))) uint16_t p0[BI * kBK];
+    __shared__ __attribute__((aligned(1024))) uint16_t p1[BI * kBK];
+    __shared__ __attribute__((aligned(1024))) uint16_t q0[BJ * kBK];
+    __shared__ __attribute__((aligned(1024))) uint16_t q1[BJ * kBK];
+
+    int ti, tj;
+    tile_of(a, ti, tj);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int wi = wave / WJ * (BI / WI), wj = wave % WJ * (BJ / WJ);
+    const int64_t i0 = static_cast<int64_t>(ti) * BI, j0 = static_cast<int64_t>(tj) * BJ;
+    const int part = blockIdx.y;
+    const int64_t c0 = part * a.chunk, c1 = min(a.nc, c0 + a.chunk);
+    const int steps = c1 > c0 ? static_cast<int>((c1 - c0 + kBK - 1) / kBK) : 0;
+
+    f32x4 acc[FI][FJ];
+    f32x4 sums[FI];
+#pragma unroll
+    for (int f = 0; f < FI; ++f) {
+        sums[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < FJ; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    // the column sums of dy are one more product, with a matrix of ones
+    const bool with_db = OP == WGRAD && a.e.db != nullptr && tj == 0 && wj == 0;
+
+    Stage<PKC, BI, THREADS> sp;
+    Stage<QKC, BJ, THREADS> sq;
+    auto load = [&](int s) {
+        sp.load(a.p, a.ldp, i0, a.ni, c0 + static_cast<int64_t>(s) * kBK, c1);
+        sq.load(a.q, a.ldq, j0, a.nj, c0 + static_cast<int64_t>(s) * kBK, c1);
+    };
+    auto compute = [&](const uint16_t *tp, const uint16_t *tq) {
+#pragma unroll
+        for (int kk = 0; kk < kBK / 32; ++kk) {
+            s16x8 fp[FI], fq[FJ];
+#pragma unroll
+            for (int t = 0; t < FJ; ++t) fq[t] = fragment<QKC, BJ>(tq, wj + t * 16, kk, lane);
+#pragma unroll
+            for (int f = 0; f < FI; ++f) fp[f] = fragment<PKC, BI>(tp, wi + f * 16, kk, lane);
+#pragma unroll
+            for (int f = 0; f < FI; ++f)
+#pragma unroll
+                for (int t = 0; t < FJ; ++t) acc[f][t] = mfma<T>(fq[t], fp[f], acc[f][t]);
+            if (OP == WGRAD && with_db) {
+                const short one = static_cast<short>(T::down(1.0f));
+                const s16x8 ones = {one, one, one, one, one, one, one, one};
+#pragma unroll
+                for (int f = 0; f < FI; ++f) sums[f] = mfma<T>(ones, fp[f], sums[f]);
+            }
+        }
+    };
+    auto step = [&](int s, const uint16_t *tp, const uint16_t *tq, uint16_t *np, uint16_t *nq) {
+        if (s + 1 < steps) load(s + 1);
+        compute(tp, tq);
+        if (s + 1 < steps) {
+            sp.store(np);
+            sq.store(nq);
+        }
+        __syncthreads();
+    };
+    if (steps > 0) {
+        load(0);
+        sp.store(p0);
+        sq.store(q0);
+        __syncthreads();
+        for (int s = 0; s < steps; s += 2) {
+            step(s, p0, q0, p1, q1);
+            if (s + 1 < steps) step(s + 1, p1, q1, p0, q0);
+        }
+    }
+
+    const int g = lane >> 4;
+    const int64_t njp = padded4(a.nj);
+    const uint64_t stream = OP != WGRAD && a.e.drop.on && a.parts == 1 ? drop_stream(a.e.drop) : 0;
+    // one body for all rows of blocks: the block's registers are selected by
+    // uniform branches
+#pragma unroll 1
+    for (int f = 0; f < FI; ++f) {
+        f32x4 v[FJ], sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < FI; ++s)
+            if (s == f) {
+                sum = sums[s];
+#pragma unroll
+                for (int t = 0; t < FJ; ++t) v[t] = acc[s][t];
+            }
+        const int64_t i = i0 + wi + f * 16 + (lane & 15);
+        if (i >= a.ni) continue;
+        if (a.parts > 1) {
+            float *row = a.partial + (part * a.ni + i) * njp;
+#pragma unroll
+            for (int t = 0; t < FJ; ++t) {
+                const int64_t j = j0 + wj + t * 16 + g * 4;
+                if (j < a.nj) *reinterpret_cast<f32x4 *>(row + j) = v[t];
+            }
+            if (OP == WGRAD && with_db && g == 0)
+                a.partial[a.parts * a.ni * njp + part * a.ni + i] = sum[0];
+            continue;
+        }
+#pragma unroll
+        for (int t = 0; t < FJ; t += 2)
+            emit_pair<OP, T>(a.e, i, j0 + wj + t * 16 + g * 4, a.nj, stream, v[t], v[t + 1]);
+        if (OP == WGRAD && with_db && g == 0) emit_db<T>(a.e, i, sum[0]);
+    }
+}
+
+// Adds the parts of a divided contraction in their order and finishes the
+// outputs; a thread has the two quads that share a draw of the mask.
+template <int OP, class T>
+__global__ void __launch_bounds__(256) join_kernel(Args a) {
+    const int64_t quads = (a.nj + 31) / 32 * 4;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (id >= a.ni * quads) return;
+    const int64_t i = id / quads, u = id - i * quads;
+    const int64_t j = u / 4 * 32 + u % 4 * 4;
+    const int64_t njp = padded4(a.nj);
+    const uint64_t stream = OP != WGRAD && a.e.drop.on ? drop_stream(a.e.drop) : 0;
+    if (j < a.nj) {
+        const bool second = j + 16 < a.nj;
+        f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
+        const float *row = a.partial + i * njp + j;
+        for (int s = 0; s < a.parts; ++s, row += a.ni * njp) {
+            v0 += *reinterpret_cast<const f32x4 *>(row);
+            if (second) v1 += *reinterpret_cast<const f32x4 *>(row + 16);
+        }
+        emit_pair<OP, T>(a.e, i, j, a.nj, stream, v0, v1);
+    }
+    if (OP == WGRAD && a.e.db != nullptr && u == 0) {
+        const float *col = a.partial + a.parts * a.ni * njp + i;
+        float v = 0.0f;
+        for (int s = 0; s < a.parts; ++s) v += col[s * a.ni];
+        emit_db<T>(a.e, i, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+constexpr int kCUs = 256;
+
+struct Plan {
+    int bi, bj, parts;
+    int64_t chunk;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+Plan plan_for(int64_t ni, int64_t nj, int64_t nc) {
+    Plan p{256, 256, 1, 0};
+    if (ceil_div(ni, 256) * ceil_div(nj, 256) < kCUs * 3 / 4) p.bi = p.bj = 128;
+    if (ni <= 64) p.bi = 64;
+    const int64_t tiles = ceil_div(ni, p.bi) * ceil_div(nj, p.bj);
+    const int64_t steps = ceil_div(nc, kBK);
+    int64_t parts = 1;
+    if (tiles < kCUs) parts = std::min<int64_t>(2 * kCUs / std::max<int64_t>(tiles, 1), steps / 4);
+    parts = std::max<int64_t>(1, std::min<int64_t>(parts, 64));
+    p.chunk = std::max<int64_t>(ceil_div(steps, parts), 1) * kBK;
+    p.parts = static_cast<int>(std::max<int64_t>(1, ceil_div(nc, p.chunk)));
+    return p;
+}
+
+int64_t partial_bytes(const Plan &p, int64_t ni, int64_t nj) {
+    return p.parts == 1 ? 0 : p.parts * ni * (padded4(nj) + 1) * 4 + 16;
+}
+
+template <int OP, class T>
+zero_status launch(Args a, void *stream) {
+    const Plan p = plan_for(a.ni, a.nj, a.nc);
+    a.chunk = p.chunk;
+    a.parts = p.parts;
+    a.tiles_i = static_cast<int32_t>(ceil_div(a.ni, p.bi));
+    a.tiles_j = static_cast<int32_t>(ceil_div(a.nj, p.bj));
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j;
+    if (tiles > 0x7FFFFFFF) return ZERO_EINVAL;
+    const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(a.parts));
+    if (p.bi == 256)
+        tile_kernel<OP, T, 256, 256, 2, 4><<<grid, 512, 0, st>>>(a);
+    else if (p.bi == 128)
+        tile_kernel<OP, T, 128, 128, 2, 2><<<grid, 256, 0, st>>>(a);
+    else
+        tile_kernel<OP, T, 64, 128, 1, 4><<<grid, 256, 0, st>>>(a);
+    if (a.parts > 1) {
+        const int64_t threads = a.ni * (ceil_div(a.nj, 32) * 4);
+        join_kernel<OP, T><<<static_cast<uint32_t>(ceil_div(threads, 256)), 256, 0, st>>>(a);
+    }
+    return launch_status();
+}
+
+template <int OP>
+zero_status launch(const Args &a, zero_dtype dt, void *stream) {
+    return dt == ZERO_BF16 ? launch<OP, BF16>(a, stream) : launch<OP, FP16>(a, stream);
+}
+
+// every row of a matrix starts at a multiple of four elements
+bool quads(const Mat &m) {
+    return m.empty() || m.p == nullptr ||
+           (reinterpret_cast<uintptr_t>(m.p) % static_cast<uintptr_t>(4 * m.elem) == 0 &&
+            (m.rows <= 1 || m.ld % 4 == 0));
+}
+
+bool workspace_ok(int64_t need, const void *ws, int64_t bytes) {
+    return need == 0 || (ws != nullptr && aligned16(ws) && bytes >= need);
+}
+
+struct Shape {
+    int64_t ni, nj, nc;
+};
+
+Shape shape_of(int op, int64_t m, int64_t n, int64_t k) {
+    if (op == FWD) return {m, n, k};
+    if (op == DGRAD) return {m, k, n};
+    return {n, k, m};
+}
+
+// linear and dgrad after their own checks: out = residual + D(f(P Q))
+template <int OP>
+zero_status product(const Mat &p, const Mat &q, zero_dtype dt, const Shape &s, const Mat &bias,
+                    zero_act act, const Mat &z, const zero_dropout_params *drop, const Mat &res,
+                    const Mat &out, void *workspace, int64_t workspace_bytes, void *stream) {
+    Args a{};
+    if (static_cast<int>(act) < ZERO_ACT_NONE || static_cast<int>(act) > ZERO_ACT_SILU)
+        return ZERO_EINVAL;
+    if (!make_drop(drop, s.ni, &a.e.drop)) return ZERO_EINVAL;
+    if (!p.ok() || !q.ok() || !out.ok() || (bias.p != nullptr && !bias.ok()) ||
+        (res.p != nullptr && !res.ok()) || (z.p != nullptr && !z.ok()))
+        return ZERO_EINVAL;
+    if (OP == DGRAD && act != ZERO_ACT_NONE && z.p == nullptr && !out.empty()) return ZERO_EINVAL;
+    if (out.empty()) return ZERO_OK;
+    const int64_t need = partial_bytes(plan_for(s.ni, s.nj, s.nc), s.ni, s.nj);
+    if (!workspace_ok(need, workspace, workspace_bytes)) return ZERO_EINVAL;
+    const bool z_out = OP == FWD;
+    const Span sp = p.span(), sq = q.span(), sb = bias.span(), sr = res.span(), so = out.span(),
+               sz = z.span(),
+               sw = need ? span_of(workspace, need, 1) : Span{0, 0},
+               st = a.e.drop.step ? span_of(a.e.drop.step, 8, 1) : Span{0, 0};
+    for (const Span &r : {sp, sq, sb, st}) {
+        if (overlap(so, r) || overlap(sw, r)) return ZERO_EALIAS;
+        if (z_out && overlap(sz, r)) return ZERO_EALIAS;
+    }
+    if (overlap(so, sz) || overlap(so, sw) || overlap(sz, sw) || overlap(sr, sw) ||
+        (z_out && overlap(sz, sr)))
+        return ZERO_EALIAS;
+    if (res.p != nullptr && overlap(so, sr) && !res.same_place(out)) return ZERO_EALIAS;
+    a.p = static_cast<const uint16_t *>(p.p);
+    a.q = static_cast<const uint16_t *>(q.p);
+    a.ldp = p.ld;
+    a.ldq = q.ld;
+    a.ni = s.ni;
+    a.nj = s.nj;
+    a.nc = s.nc;
+    a.partial = static_cast<float *>(workspace);
+    a.e.bias = static_cast<const uint16_t *>(bias.p);
+    a.e.res = res.p;
+    a.e.ldr = res.ld;
+    a.e.out = const_cast<void *>(out.p);
+    a.e.ldo = out.ld;
+    a.e.z = static_cast<uint16_t *>(const_cast<void *>(z.p));
+    a.e.ldz = z.ld;
+    a.e.act = act;
+    a.e.out_f32 = out.elem == 4;
+    a.e.vec = quads(out) && quads(res) && quads(z) && quads(bias);
+    return launch<OP>(a, dt, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t zero_linear_workspace_bytes(zero_linear_op op, int64_t m, int64_t n, int64_t k) {
+    if (static_cast<int>(op) < FWD || static_cast<int>(op) > WGRAD || !dim_ok(m) || !dim_ok(n) ||
+        !dim_ok(k))
+        return -1;
+    const Shape s = shape_of(op, m, n, k);
+    if (s.ni == 0 || s.nj == 0) return 0;
+    return partial_bytes(plan_for(s.ni, s.nj, s.nc), s.ni, s.nj);
+}
+
+zero_status zero_linear(const void *x, zero_dtype dt, int64_t ldx, const void *w, int64_t ldw,
+                        const void *bias, int64_t m, int64_t n, int64_t k, zero_act act,
+                        const zero_dropout_params *drop, const void *residual, int64_t ldr,
+                        void *y, zero_dtype ydt, int64_t ldy, void *z, int64_t ldz,
+                        void *workspace, int64_t workspace_bytes, void *stream) {
+    if (!is16(dt) || !(ydt == dt || ydt == ZERO_FP32) || !dim_ok(m) || !dim_ok(n) || !dim_ok(k))
+        return ZERO_EINVAL;
+    const int64_t ye = size_of(ydt);
+    return product<FWD>(Mat{x, m, k, ldx, 2}, Mat{w, n, k, ldw, 2}, dt, Shape{m, n, k},
+                        Mat{bias, 1, n, n, 2}, act, Mat{z, m, n, ldz, 2}, drop,
+                        Mat{residual, m, n, ldr, ye}, Mat{y, m, n, ldy, ye}, workspace,
+                        workspace_bytes, stream);
+}
+
+zero_status zero_linear_dgrad(const void *dy, zero_dtype dt, int64_t lddy, const void *w,
+                              int64_t ldw, int64_t m, int64_t n, int64_t k, zero_act act,
+                              const void *z, int64_t ldz, const zero_dropout_params *drop,
+                              const void *residual, int64_t ldr, void *dx, zero_dtype dxdt,
+                              int64_t lddx, void *workspace, int64_t workspace_bytes,
+                              void *stream) {
+    if (!is16(dt) || !(dxdt == dt || dxdt == ZERO_FP32) || !dim_ok(m) || !dim_ok(n) || !dim_ok(k))
+        return ZERO_EINVAL;
+    const int64_t xe = size_of(dxdt);
+    return product<DGRAD>(Mat{dy, m, n, lddy, 2}, Mat{w, n, k, ldw, 2}, dt, Shape{m, k, n},
+                          Mat{nullptr, 1, k, k, 2}, act,
+                          Mat{act == ZERO_ACT_NONE ? nullptr : z, m, k, ldz, 2}, drop,
+                          Mat{residual, m, k, ldr, xe}, Mat{dx, m, k, lddx, xe}, workspace,
+                          workspace_bytes, stream);
+}
+
+zero_status zero_linear_wgrad(const void *dy, zero_dtype dt, int64_t lddy, const void *x,
+                              int64_t ldx, int64_t m, int64_t n, int64_t k, void *dw,
+                              zero_dtype gdt, int64_t lddw, void *db, int32_t accumulate,
+                              void *workspace, int64_t workspace_bytes, void *stream) {
+    if (!is16(dt) || !(gdt == dt || gdt == ZERO_FP32) || !dim_ok(m) || !dim_ok(n) || !dim_ok(k))
+        return ZERO_EINVAL;
+    const int64_t ge = size_of(gdt);
+    const Mat my{dy, m, n, lddy, 2}, mx{x, m, k, ldx, 2}, mw{dw, n, k, lddw, ge},
+        mb{db, 1, n, n, ge};
+    if (!my.ok() || !mx.ok() || !mw.ok() || (db != nullptr && !mb.ok())) return ZERO_EINVAL;
+    if (n == 0 || k == 0) {
+        // no column of dW: a bias gradient still has its sums
+        if (n == 0 || db == nullptr) return ZERO_OK;
+        return ZERO_EINVAL;
+    }
+    const Shape s = shape_of(WGRAD, m, n, k);
+    const int64_t need = partial_bytes(plan_for(s.ni, s.nj, s.nc), s.ni, s.nj);
+    if (!workspace_ok(need, workspace, workspace_bytes)) return ZERO_EINVAL;
+    const Span sy = my.span(), sx = mx.span(), sd = mw.span(), sb = mb.span(),
+               sw = need ? span_of(workspace, need, 1) : Span{0, 0};
+    for (const Span &r : {sy, sx})
+        if (overlap(sd, r) || overlap(sb, r) || overlap(sw, r)) return ZERO_EALIAS;
+    if (overlap(sd, sb) || overlap(sd, sw) || overlap(sb, sw)) return ZERO_EALIAS;
+    Args a{};
+    a.p = static_cast<const uint16_t *>(dy);
+    a.q = static_cast<const uint16_t *>(x);
+    a.ldp = lddy;
+    a.ldq = ldx;
+    a.ni = s.ni;
+    a.nj = s.nj;
+    a.nc = s.nc;
+    a.partial = static_cast<float *>(workspace);
+    a.e.out = dw;
+    a.e.ldo = lddw;
+    a.e.out_f32 = gdt == ZERO_FP32;
+    a.e.db = db;
+    a.e.accumulate = accumulate != 0;
+    a.e.vec = quads(mw);
+    return launch<WGRAD>(a, dt, stream);
+}
+
+}  // extern "C"

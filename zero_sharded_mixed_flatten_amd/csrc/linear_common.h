@@ -1,0 +1,246 @@
+// linear_common.h -- device and host pieces shared by the layer products
+// (linear.hip) and the dropout (dropout.hip): the counter-based mask, the
+// activations, 16-bit conversions, argument checks.  Internal.
+#ifndef ZERO_SHARD_LINEAR_COMMON_H
+#define ZERO_SHARD_LINEAR_COMMON_H
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "host_common.h"
+#include "zero_linear.h"
+
+namespace zero_linear_impl {
+
+using f32x4 = float __attribute__((ext_vector_type(4)));
+using f32x2 = float __attribute__((ext_vector_type(2)));
+using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+using u16x4 = uint16_t __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------------------
+// 16-bit element types
+
+struct BF16 {
+    using elem = __bf16;
+    static __device__ __forceinline__ float up(uint16_t h) {
+        return __builtin_bit_cast(float, static_cast<uint32_t>(h) << 16);
+    }
+    static __device__ __forceinline__ uint16_t down(float f) {
+        return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+    }
+};
+struct FP16 {
+    using elem = _Float16;
+    static __device__ __forceinline__ float up(uint16_t h) {
+        return static_cast<float>(__builtin_bit_cast(_Float16, h));
+    }
+    static __device__ __forceinline__ uint16_t down(float f) {
+        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
+    }
+};
+
+// four elements as fp32, and back; n < 4 touches the first n only
+template <class T>
+__device__ __forceinline__ f32x4 load16(const uint16_t *p, int n, bool vec) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (vec && n == 4) {
+        const u16x4 h = *reinterpret_cast<const u16x4 *>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = T::up(h[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) v[e] = T::up(p[e]);
+    }
+    return v;
+}
+
+template <class T>
+__device__ __forceinline__ void store16(uint16_t *p, f32x4 v, int n, bool vec) {
+    u16x4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = T::down(v[e]);
+    if (vec && n == 4) {
+        *reinterpret_cast<u16x4 *>(p) = h;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) p[e] = h[e];
+    }
+}
+
+__device__ __forceinline__ f32x4 load32(const float *p, int n, bool vec) {
+    if (vec && n == 4) return *reinterpret_cast<const f32x4 *>(p);
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < n) v[e] = p[e];
+    return v;
+}
+
+__device__ __forceinline__ void store32(float *p, f32x4 v, int n, bool vec) {
+    if (vec && n == 4) {
+        *reinterpret_cast<f32x4 *>(p) = v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) p[e] = v[e];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dropout
+
+struct Drop {
+    uint32_t on, threshold, k0, k1, row0;
+    float scale;
+    uint64_t offset;
+    const int64_t *step;
+};
+
+// Philox4x32-10 (the generator of Salmon et al., 2011): ten rounds of two
+// 32 x 32 -> 64 bit products.  Integer work of about 20 full products for
+// eight mask elements.
+__device__ __forceinline__ u32x4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3,
+                                        uint32_t k0, uint32_t k1) {
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0;
+        const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
+        c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
+        c1 = static_cast<uint32_t>(p1);
+        c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
+        c3 = static_cast<uint32_t>(p0);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return u32x4{c0, c1, c2, c3};
+}
+
+__device__ __forceinline__ uint64_t drop_stream(const Drop &d) {
+    return d.offset + (d.step != nullptr ? static_cast<uint64_t>(*d.step) : 0u);
+}
+
+// The words of (row, block).  One call serves the columns 4b..4b+3 (low
+// halves) and 16+4b..16+4b+3 (high halves) of a 32-column group, which is
+// what a lane of the products holds of two neighbouring 16 x 16 tiles: no
+// random bit is drawn twice or thrown away in either kernel.
+__device__ __forceinline__ u32x4 drop_words(const Drop &d, uint64_t stream, uint32_t row,
+                                            uint32_t block) {
+    return philox(block, d.row0 + row, static_cast<uint32_t>(stream),
+                  static_cast<uint32_t>(stream >> 32), d.k0, d.k1);
+}
+
+__device__ __forceinline__ f32x4 drop_apply(const Drop &d, u32x4 w, int half, f32x4 v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t u = half ? w[e] >> 16 : w[e] & 0xFFFFu;
+        v[e] = u >= d.threshold ? v[e] * d.scale : 0.0f;
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// activations (fp32).  Sigmoids are 1 / (1 + 2^(-u log2 e)) by the hardware's
+// exp2 and reciprocal, each good to about an ulp: a relative error of some
+// 2^-22, below the half step 2^-11 of the finest 16-bit output; with an fp32
+// output it is the largest error of the call.
+
+__device__ __forceinline__ float sigmoid(float u) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f));
+}
+
+__device__ __forceinline__ float act_value(float v, int act) {
+    switch (act) {
+        case ZERO_ACT_RELU: return v > 0.0f ? v : (v != v ? v : 0.0f);
+        case ZERO_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+        case ZERO_ACT_GELU_TANH:  // (1 + tanh(u / 2)) / 2 = sigmoid(u)
+            return v * sigmoid(1.5957691216057308f * (v + 0.044715f * (v * v * v)));
+        case ZERO_ACT_SILU: return v * sigmoid(v);
+        default: return v;
+    }
+}
+
+// Where the bell factor of a derivative has vanished its product with v is 0
+// (0 * Inf would not be).
+__device__ __forceinline__ float act_slope(float v, int act) {
+    float s, t, d;
+    switch (act) {
+        case ZERO_ACT_GELU:
+            s = 0.5f * (1.0f + erff(v * 0.70710678118654752f));
+            t = __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f);
+            d = v * 0.39894228040143268f;
+            break;
+        case ZERO_ACT_GELU_TANH:
+            s = sigmoid(1.5957691216057308f * (v + 0.044715f * (v * v * v)));
+            t = s * (1.0f - s);
+            d = v * (1.5957691216057308f * (1.0f + 0.134145f * (v * v)));
+            break;
+        default:  // SILU
+            s = sigmoid(v);
+            t = s * (1.0f - s);
+            d = v;
+            break;
+    }
+    return t == 0.0f ? s : s + t * d;
+}
+
+// ---------------------------------------------------------------------------
+// host: arguments
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
+constexpr int64_t kMaxSpan = int64_t(1) << 60;
+
+inline bool is16(zero_dtype t) { return t == ZERO_BF16 || t == ZERO_FP16; }
+inline int64_t size_of(zero_dtype t) { return t == ZERO_FP32 ? 4 : 2; }
+
+// one matrix argument: its checks and its span in memory
+struct Mat {
+    const void *p;
+    int64_t rows, cols, ld, elem;
+    bool empty() const { return rows == 0 || cols == 0; }
+    // elements from the first to one past the last
+    int64_t extent() const { return empty() ? 0 : (rows - 1) * ld + cols; }
+    bool ok() const {
+        if (ld < cols) return false;
+        if (empty()) return true;
+        if (p == nullptr || reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(elem) != 0)
+            return false;
+        return rows == 1 || ld <= (kMaxSpan - cols) / (rows - 1);
+    }
+    zero_host::Span span() const {
+        return p == nullptr ? zero_host::Span{0, 0} : zero_host::span_of(p, extent(), elem);
+    }
+    bool same_place(const Mat &o) const {
+        return p == o.p && (ld == o.ld || rows <= 1) && elem == o.elem;
+    }
+};
+
+inline bool dim_ok(int64_t d) { return d >= 0 && d <= kMaxDim; }
+
+// EINVAL for parameters out of their domain; fills *out (off for a NULL
+// struct or a threshold of zero)
+inline bool make_drop(const zero_dropout_params *d, int64_t rows, Drop *out) {
+    *out = Drop{};
+    if (d == nullptr) return true;
+    if (!(d->p >= 0.0 && d->p < 1.0) || d->row0 < 0 || d->row0 > (int64_t(1) << 32) - rows ||
+        (reinterpret_cast<uintptr_t>(d->step) & 7u) != 0)
+        return false;
+    const double t = std::rint(d->p * 65536.0);
+    out->threshold = t > 65535.0 ? 65535u : static_cast<uint32_t>(t);
+    out->on = out->threshold != 0;
+    out->scale = static_cast<float>(65536.0 / (65536.0 - out->threshold));
+    out->k0 = static_cast<uint32_t>(d->seed);
+    out->k1 = static_cast<uint32_t>(d->seed >> 32);
+    out->row0 = static_cast<uint32_t>(d->row0);
+    out->offset = d->offset;
+    out->step = out->on ? d->step : nullptr;
+    return true;
+}
+
+}  // namespace zero_linear_impl
+
+#endif
