@@ -154,14 +154,25 @@ __device__ __forceinline__ void emit_db(const Epilogue &e, int64_t i, float v) {
 // lane's operand is one piece, eight consecutive c of its row.  The exclusive
 // or spreads the pieces that eight lanes read at once over all banks.
 //
-// Rows of lanes: [64][ROWS], piece (c, s) at c * ROWS / 8 + (s ^ 2 (c & M)),
-// M = 7 (3 for 64 lanes): 32-byte units of 16 lanes stay whole and those of
-// neighbouring c fall into different banks.  ds_read_b64_tr_b16 reads four
-// rows of such a unit and hands every lane the four c of its own column: two
-// of them make an operand.
+// Rows of lanes: [64][ROWS], in 32-byte units of 16 lanes.
+// ds_read_b64_tr_b16 reads four rows of a unit and hands every lane the four
+// c of its own column; two of them make an operand.  The four rows must lie
+// in different banks: unit u of row c is stored at u ^ flip(c), and tiles of
+// 256 lanes, whose rows are two bank widths long, also skip 32 bytes after
+// each 1024 (a wave's direct copy is 1024 bytes, so it is not cut).  flip
+// touches few bits and depends on c mod 4 only, so that a lane's addresses
+// are one or two registers plus constants.
 
 template <int ROWS>
-constexpr int kSwizzle = ROWS >= 128 ? 7 : 3;
+constexpr int kFlipBits = ROWS == 256 ? 4 : ROWS == 128 ? 6 : 1;
+template <int ROWS>
+__device__ __forceinline__ int flip(int c) {
+    return ROWS == 256 ? (c & 1) * 4 : ROWS == 128 ? (c & 3) * 2 : (c >> 1) & 1;
+}
+template <bool KC, int ROWS>
+constexpr int kSkip = !KC && ROWS == 256 ? 16 : 0;  // elements after each 512
+template <bool KC, int ROWS>
+constexpr int kTile = ROWS * kBK + ROWS * kBK / 512 * kSkip<KC, ROWS>;
 
 template <bool KC, int ROWS>
 __device__ __forceinline__ int piece_row(int pos) {
@@ -170,7 +181,13 @@ __device__ __forceinline__ int piece_row(int pos) {
 template <bool KC, int ROWS>
 __device__ __forceinline__ int piece_slot(int pos) {
     if (KC) return (pos & 7) ^ ((pos >> 3) & 7);
-    return (pos % (ROWS / 8)) ^ (2 * ((pos / (ROWS / 8)) & kSwizzle<ROWS>));
+    return (pos % (ROWS / 8)) ^ (2 * flip<ROWS>(pos / (ROWS / 8)));
+}
+
+// where piece pos lies in the tile
+template <bool KC, int ROWS>
+__device__ __forceinline__ int piece_at(int pos) {
+    return pos * 8 + (pos >> 6) * kSkip<KC, ROWS>;
 }
 
 // A piece of the operand as eight elements, zeros past the row's or the
@@ -212,31 +229,71 @@ struct Stage {
     __device__ __forceinline__ void store(uint16_t *tile) const {
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            *reinterpret_cast<u32x4 *>(tile + (n * THREADS + static_cast<int>(threadIdx.x)) * 8) =
-                v[n];
+            *reinterpret_cast<u32x4 *>(
+                tile + piece_at<KC, ROWS>(n * THREADS + static_cast<int>(threadIdx.x))) = v[n];
     }
 };
 
-// a lane's operand of a 16-row block: eight consecutive c from kk * 32 on
+// Direct copies of whole steps from global memory into a tile: a wave's 64
+// pieces of one instruction land at consecutive places, so the exclusive or
+// is applied to where each lane reads instead.  Rows past the operand's last
+// read that row again (their outputs are never stored).
+template <bool KC, int ROWS, int THREADS>
+struct Direct {
+    static constexpr int N = ROWS * kBK / 8 / THREADS;
+    const char *base;       // of the next step
+    int64_t stride;         // bytes from step to step
+    uint32_t off[N];
+    __device__ __forceinline__ void init(const uint16_t *p, int64_t ld, int64_t r0, int64_t rows,
+                                         int64_t c0) {
+        base = reinterpret_cast<const char *>(KC ? p + r0 * ld + c0 : p + c0 * ld + r0);
+        stride = (KC ? kBK : kBK * ld) * 2;
+        const int last = static_cast<int>(min(rows - r0, static_cast<int64_t>(ROWS))) - (KC ? 1 : 8);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int pos = n * THREADS + static_cast<int>(threadIdx.x);
+            const int row = piece_row<KC, ROWS>(pos), s = piece_slot<KC, ROWS>(pos);
+            off[n] = KC ? static_cast<uint32_t>(min(row, last)) * static_cast<uint32_t>(ld * 2) + s * 16
+                        : static_cast<uint32_t>(row) * static_cast<uint32_t>(ld * 2) +
+                              min(s * 8, last) * 2;
+        }
+    }
+    __device__ __forceinline__ void issue(uint16_t *tile, int wave) {
+        using g32 = const __attribute__((address_space(1))) uint32_t;
+        using l32 = __attribute__((address_space(3))) uint32_t;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            __builtin_amdgcn_global_load_lds((g32 *)(base + off[n]),
+                                             (l32 *)(tile + piece_at<KC, ROWS>(n * THREADS + wave * kWave)),
+                                             16, 0, 0);
+        base += stride;
+    }
+};
+
+// a lane's operand of 16-row block f from row row0 on: eight consecutive c
+// from kk * 32 on
 template <bool KC, int ROWS>
-__device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int kk, int lane) {
+__device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int f, int kk, int lane) {
     if constexpr (KC) {
         const int r = lane & 15, s = kk * 4 + (lane >> 4);
-        return *reinterpret_cast<const s16x8 *>(tile + (row0 + r) * kBK + ((s ^ (r & 7)) * 8));
+        return *reinterpret_cast<const s16x8 *>(tile + (row0 + r) * kBK + ((s ^ (r & 7)) * 8) +
+                                                f * 16 * kBK);
     } else {
-        const int t = lane & 15, g = lane >> 4;
+        const int t = lane & 15, c = (lane >> 4) * 8 + (t >> 2);
+        constexpr int F = kFlipBits<ROWS>;
+        const int at = c * ROWS + (c * ROWS >> 9) * kSkip<KC, ROWS> +
+                       ((row0 / 16 + (f & F)) ^ flip<ROWS>(c)) * 16 + (t & 3) * 4;
         using lds4 = __attribute__((address_space(3))) s16x4;
-        s16x8 f;
+        s16x8 v;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int c = kk * 32 + g * 8 + h * 4 + (t >> 2);
-            const int unit = (row0 >> 4) ^ (c & kSwizzle<ROWS>);
-            const uint16_t *a = tile + c * ROWS + unit * 16 + (t & 3) * 4;
-            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(a));
+            constexpr int per_row = ROWS + ROWS * kSkip<KC, ROWS> / 512;
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds4 *)(tile + at + (f & ~F) * 16 + (kk * 32 + h * 4) * per_row));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[h * 4 + e] = x[e];
+            for (int e = 0; e < 4; ++e) v[h * 4 + e] = x[e];
         }
-        return f;
+        return v;
     }
 }
 
@@ -253,16 +310,16 @@ __device__ __forceinline__ void tile_of(const Args &a, int &ti, int &tj) {
     tj = in / high;
 }
 
-template <int OP, class T, int BI, int BJ, int WI, int WJ>
+template <int OP, class T, int BI, int BJ, int WI, int WJ, bool DIRECT>
 __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     constexpr bool PKC = OP != WGRAD, QKC = OP == FWD;
     constexpr int THREADS = WI * WJ * kWave;
     constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
     static_assert(FJ % 2 == 0, "mask draws pair two 16-column blocks");
-    __shared__ __attribute__((aligned(1024))) uint16_t p0[BI * kBK];
-    __shared__ __attribute__((aligned(1024))) uint16_t p1[BI * kBK];
-    __shared__ __attribute__((aligned(1024))) uint16_t q0[BJ * kBK];
-    __shared__ __attribute__((aligned(1024))) uint16_t q1[BJ * kBK];
+    __shared__ __attribute__((aligned(1024))) uint16_t p0[kTile<PKC, BI>];
+    __shared__ __attribute__((aligned(1024))) uint16_t p1[kTile<PKC, BI>];
+    __shared__ __attribute__((aligned(1024))) uint16_t q0[kTile<QKC, BJ>];
+    __shared__ __attribute__((aligned(1024))) uint16_t q1[kTile<QKC, BJ>];
 
     int ti, tj;
     tile_of(a, ti, tj);
@@ -275,56 +332,79 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     const int steps = c1 > c0 ? static_cast<int>((c1 - c0 + kBK - 1) / kBK) : 0;
 
     f32x4 acc[FI][FJ];
-    f32x4 sums[FI];
 #pragma unroll
-    for (int f = 0; f < FI; ++f) {
-        sums[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int f = 0; f < FI; ++f)
 #pragma unroll
         for (int t = 0; t < FJ; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    // the column sums of dy are one more product, with a matrix of ones
+    // The column sums of dy are one more product: block f's operand with a
+    // matrix whose row f is ones, so that one accumulator's 16 rows hold the
+    // sums of all FI blocks.
+    f32x4 sums = {0.f, 0.f, 0.f, 0.f};
+    static_assert(FI <= 16, "a row of the sums for every block");
     const bool with_db = OP == WGRAD && a.e.db != nullptr && tj == 0 && wj == 0;
 
     Stage<PKC, BI, THREADS> sp;
     Stage<QKC, BJ, THREADS> sq;
-    auto load = [&](int s) {
+    auto load = [&](int s) __attribute__((always_inline)) {
         sp.load(a.p, a.ldp, i0, a.ni, c0 + static_cast<int64_t>(s) * kBK, c1);
         sq.load(a.q, a.ldq, j0, a.nj, c0 + static_cast<int64_t>(s) * kBK, c1);
     };
-    auto compute = [&](const uint16_t *tp, const uint16_t *tq) {
+    auto compute = [&](const uint16_t *tp, const uint16_t *tq) __attribute__((always_inline)) {
 #pragma unroll
         for (int kk = 0; kk < kBK / 32; ++kk) {
             s16x8 fp[FI], fq[FJ];
 #pragma unroll
-            for (int t = 0; t < FJ; ++t) fq[t] = fragment<QKC, BJ>(tq, wj + t * 16, kk, lane);
+            for (int t = 0; t < FJ; ++t) fq[t] = fragment<QKC, BJ>(tq, wj, t, kk, lane);
 #pragma unroll
-            for (int f = 0; f < FI; ++f) fp[f] = fragment<PKC, BI>(tp, wi + f * 16, kk, lane);
+            for (int f = 0; f < FI; ++f) fp[f] = fragment<PKC, BI>(tp, wi, f, kk, lane);
 #pragma unroll
             for (int f = 0; f < FI; ++f)
 #pragma unroll
                 for (int t = 0; t < FJ; ++t) acc[f][t] = mfma<T>(fq[t], fp[f], acc[f][t]);
             if (OP == WGRAD && with_db) {
-                const short one = static_cast<short>(T::down(1.0f));
-                const s16x8 ones = {one, one, one, one, one, one, one, one};
 #pragma unroll
-                for (int f = 0; f < FI; ++f) sums[f] = mfma<T>(ones, fp[f], sums[f]);
+                for (int f = 0; f < FI; ++f) {
+                    const short o = (lane & 15) == f ? static_cast<short>(T::down(1.0f)) : short(0);
+                    sums = mfma<T>(s16x8{o, o, o, o, o, o, o, o}, fp[f], sums);
+                }
             }
         }
     };
-    auto step = [&](int s, const uint16_t *tp, const uint16_t *tq, uint16_t *np, uint16_t *nq) {
-        if (s + 1 < steps) load(s + 1);
-        compute(tp, tq);
-        if (s + 1 < steps) {
-            sp.store(np);
-            sq.store(nq);
+    // whole steps go straight to shared memory; a last broken one is staged
+    const int whole = DIRECT ? static_cast<int>((c1 - c0) / kBK) : 0;
+    Direct<PKC, BI, THREADS> dp;
+    Direct<QKC, BJ, THREADS> dq;
+    if (DIRECT) {
+        dp.init(a.p, a.ldp, i0, a.ni, c0);
+        dq.init(a.q, a.ldq, j0, a.nj, c0);
+    }
+    auto put = [&](uint16_t *np, uint16_t *nq) __attribute__((always_inline)) {
+        sp.store(np);
+        sq.store(nq);
+    };
+    auto fetch = [&](int s, uint16_t *np, uint16_t *nq) __attribute__((always_inline)) {
+        if (s < whole) {
+            dp.issue(np, wave);
+            dq.issue(nq, wave);
+        } else if (s < steps) {
+            load(s);
+            if (DIRECT) put(np, nq);
         }
+    };
+    auto sync = [&]() __attribute__((always_inline)) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the direct copies have landed
         __syncthreads();
     };
+    auto step = [&](int s, const uint16_t *tp, const uint16_t *tq, uint16_t *np, uint16_t *nq) __attribute__((always_inline)) {
+        fetch(s + 1, np, nq);
+        compute(tp, tq);
+        if (!DIRECT && s + 1 < steps) put(np, nq);
+        sync();
+    };
     if (steps > 0) {
-        load(0);
-        sp.store(p0);
-        sq.store(q0);
-        __syncthreads();
+        fetch(0, p0, q0);
+        if (!DIRECT) put(p0, q0);
+        sync();
         for (int s = 0; s < steps; s += 2) {
             step(s, p0, q0, p1, q1);
             if (s + 1 < steps) step(s + 1, p1, q1, p0, q0);
@@ -334,15 +414,17 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     const int g = lane >> 4;
     const int64_t njp = padded4(a.nj);
     const uint64_t stream = OP != WGRAD && a.e.drop.on && a.parts == 1 ? drop_stream(a.e.drop) : 0;
+    auto sum_of = [&](int f) __attribute__((always_inline)) {
+        return (f & 2) ? ((f & 1) ? sums[3] : sums[2]) : ((f & 1) ? sums[1] : sums[0]);
+    };
     // one body for all rows of blocks: the block's registers are selected by
     // uniform branches
 #pragma unroll 1
     for (int f = 0; f < FI; ++f) {
-        f32x4 v[FJ], sum = {0.f, 0.f, 0.f, 0.f};
+        f32x4 v[FJ];
 #pragma unroll
         for (int s = 0; s < FI; ++s)
             if (s == f) {
-                sum = sums[s];
 #pragma unroll
                 for (int t = 0; t < FJ; ++t) v[t] = acc[s][t];
             }
@@ -355,14 +437,14 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
                 const int64_t j = j0 + wj + t * 16 + g * 4;
                 if (j < a.nj) *reinterpret_cast<f32x4 *>(row + j) = v[t];
             }
-            if (OP == WGRAD && with_db && g == 0)
-                a.partial[a.parts * a.ni * njp + part * a.ni + i] = sum[0];
+            if (OP == WGRAD && with_db && g == f >> 2)
+                a.partial[a.parts * a.ni * njp + part * a.ni + i] = sum_of(f);
             continue;
         }
 #pragma unroll
         for (int t = 0; t < FJ; t += 2)
             emit_pair<OP, T>(a.e, i, j0 + wj + t * 16 + g * 4, a.nj, stream, v[t], v[t + 1]);
-        if (OP == WGRAD && with_db && g == 0) emit_db<T>(a.e, i, sum[0]);
+        if (OP == WGRAD && with_db && g == f >> 2) emit_db<T>(a.e, i, sum_of(f));
     }
 }
 
@@ -425,23 +507,43 @@ int64_t partial_bytes(const Plan &p, int64_t ni, int64_t nj) {
     return p.parts == 1 ? 0 : p.parts * ni * (padded4(nj) + 1) * 4 + 16;
 }
 
+// Direct copies move 16-byte pieces: every row 16-byte aligned, and (rows of
+// lanes) a whole number of pieces long; a tile's rows span less than 2^32
+// bytes.
+bool direct_ok(const uint16_t *p, int64_t ld, int64_t lanes) {
+    return aligned16(p) && ld % 8 == 0 && lanes % 8 == 0 && ld < (int64_t(1) << 22);
+}
+
+template <int OP, class T, int BI, int BJ, int WI, int WJ, bool DIRECT>
+zero_status run_tiles(Args &a, hipStream_t st) {
+    a.tiles_i = static_cast<int32_t>(ceil_div(a.ni, BI));
+    a.tiles_j = static_cast<int32_t>(ceil_div(a.nj, BJ));
+    const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j;
+    if (tiles > 0x7FFFFFFF) return ZERO_EINVAL;
+    const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(a.parts));
+    tile_kernel<OP, T, BI, BJ, WI, WJ, DIRECT><<<grid, WI * WJ * kWave, 0, st>>>(a);
+    return launch_status();
+}
+
 template <int OP, class T>
 zero_status launch(Args a, void *stream) {
     const Plan p = plan_for(a.ni, a.nj, a.nc);
     a.chunk = p.chunk;
     a.parts = p.parts;
-    a.tiles_i = static_cast<int32_t>(ceil_div(a.ni, p.bi));
-    a.tiles_j = static_cast<int32_t>(ceil_div(a.nj, p.bj));
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j;
-    if (tiles > 0x7FFFFFFF) return ZERO_EINVAL;
-    const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(a.parts));
-    if (p.bi == 256)
-        tile_kernel<OP, T, 256, 256, 2, 4><<<grid, 512, 0, st>>>(a);
+    const bool d = direct_ok(a.p, a.ldp, OP == WGRAD ? a.ni : 0) &&
+                   direct_ok(a.q, a.ldq, OP == FWD ? 0 : a.nj);
+    zero_status status;
+    if (p.bi == 64)
+        status = d ? run_tiles<OP, T, 64, 128, 1, 4, true>(a, st)
+                   : run_tiles<OP, T, 64, 128, 1, 4, false>(a, st);
+    else if (!d)
+        status = run_tiles<OP, T, 128, 128, 2, 2, false>(a, st);
     else if (p.bi == 128)
-        tile_kernel<OP, T, 128, 128, 2, 2><<<grid, 256, 0, st>>>(a);
+        status = run_tiles<OP, T, 128, 128, 2, 2, true>(a, st);
     else
-        tile_kernel<OP, T, 64, 128, 1, 4><<<grid, 256, 0, st>>>(a);
+        status = run_tiles<OP, T, 256, 256, 2, 4, true>(a, st);
+    if (status != ZERO_OK) return status;
     if (a.parts > 1) {
         const int64_t threads = a.ni * (ceil_div(a.nj, 32) * 4);
         join_kernel<OP, T><<<static_cast<uint32_t>(ceil_div(threads, 256)), 256, 0, st>>>(a);
