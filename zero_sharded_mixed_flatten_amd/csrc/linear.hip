@@ -26,7 +26,8 @@ using namespace zero_linear_impl;
 using s16x4 = short __attribute__((ext_vector_type(4)));
 using s16x8 = short __attribute__((ext_vector_type(8)));
 
-constexpr int kBK = 64;  // contraction elements of one step
+constexpr int kBK = 32;    // contraction elements of one step
+constexpr int kSlots = 4;  // steps in shared memory
 
 enum Op { FWD = ZERO_LINEAR, DGRAD = ZERO_LINEAR_DGRAD, WGRAD = ZERO_LINEAR_WGRAD };
 
@@ -46,7 +47,7 @@ struct Args {
     const uint16_t *p, *q;
     int64_t ldp, ldq;
     int64_t ni, nj, nc;
-    int64_t chunk;    // contraction elements of a part, a multiple of kBK
+    int64_t chunk;    // contraction elements of a part, a multiple of 2 kBK
     int32_t parts;
     int32_t tiles_i, tiles_j;
     float *partial;   // [parts][ni][njp], then the column sums [parts][ni]
@@ -150,11 +151,11 @@ __device__ __forceinline__ void emit_db(const Epilogue &e, int64_t i, float v) {
 // ---------------------------------------------------------------------------
 // tiles in shared memory, in 16-byte pieces of eight elements
 //
-// Rows of c: [ROWS][64], piece (row, s) at row * 8 + (s ^ (row & 7)); a
+// Rows of c: [ROWS][32], piece (row, s) at row * 4 + (s ^ (row / 2 & 3)); a
 // lane's operand is one piece, eight consecutive c of its row.  The exclusive
 // or spreads the pieces that eight lanes read at once over all banks.
 //
-// Rows of lanes: [64][ROWS], in 32-byte units of 16 lanes.
+// Rows of lanes: [32][ROWS], in 32-byte units of 16 lanes.
 // ds_read_b64_tr_b16 reads four rows of a unit and hands every lane the four
 // c of its own column; two of them make an operand.  The four rows must lie
 // in different banks: unit u of row c is stored at u ^ flip(c), and tiles of
@@ -176,11 +177,11 @@ constexpr int kTile = ROWS * kBK + ROWS * kBK / 512 * kSkip<KC, ROWS>;
 
 template <bool KC, int ROWS>
 __device__ __forceinline__ int piece_row(int pos) {
-    return KC ? pos >> 3 : pos / (ROWS / 8);
+    return KC ? pos >> 2 : pos / (ROWS / 8);
 }
 template <bool KC, int ROWS>
 __device__ __forceinline__ int piece_slot(int pos) {
-    if (KC) return (pos & 7) ^ ((pos >> 3) & 7);
+    if (KC) return (pos & 3) ^ ((pos >> 3) & 3);
     return (pos % (ROWS / 8)) ^ (2 * flip<ROWS>(pos / (ROWS / 8)));
 }
 
@@ -209,6 +210,7 @@ __device__ __forceinline__ u32x4 load_piece(const uint16_t *p, int64_t n) {
 template <bool KC, int ROWS, int THREADS>
 struct Stage {
     static constexpr int N = ROWS * kBK / 8 / THREADS;
+    static_assert(N >= 1 && N * THREADS * 8 == ROWS * kBK, "whole pieces for every thread");
     u32x4 v[N];
     // rows [r0, rows), contraction [c0, c1)
     __device__ __forceinline__ void load(const uint16_t *p, int64_t ld, int64_t r0, int64_t rows,
@@ -237,7 +239,10 @@ struct Stage {
 // Direct copies of whole steps from global memory into a tile: a wave's 64
 // pieces of one instruction land at consecutive places, so the exclusive or
 // is applied to where each lane reads instead.  Rows past the operand's last
-// read that row again (their outputs are never stored).
+// read that row again (their outputs are never stored).  The instruction is
+// written out because the compiler makes every later read of shared memory
+// wait for all copies it knows of; the kernel waits for the ones it needs.
+// It has no output register, and its inputs are read when it issues.
 template <bool KC, int ROWS, int THREADS>
 struct Direct {
     static constexpr int N = ROWS * kBK / 8 / THREADS;
@@ -258,25 +263,25 @@ struct Direct {
                               min(s * 8, last) * 2;
         }
     }
-    __device__ __forceinline__ void issue(uint16_t *tile, int wave) {
-        using g32 = const __attribute__((address_space(1))) uint32_t;
-        using l32 = __attribute__((address_space(3))) uint32_t;
+    // tile: its byte address in shared memory
+    __device__ __forceinline__ void issue(uint32_t tile, int wave) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            __builtin_amdgcn_global_load_lds((g32 *)(base + off[n]),
-                                             (l32 *)(tile + piece_at<KC, ROWS>(n * THREADS + wave * kWave)),
-                                             16, 0, 0);
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                         :
+                         : "s"(tile + 2 * piece_at<KC, ROWS>(n * THREADS + wave * kWave)),
+                           "v"(off[n]), "s"(base)
+                         : "memory", "m0");
         base += stride;
     }
 };
 
-// a lane's operand of 16-row block f from row row0 on: eight consecutive c
-// from kk * 32 on
+// a lane's operand of 16-row block f from row row0 on: its eight consecutive c
 template <bool KC, int ROWS>
-__device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int f, int kk, int lane) {
+__device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int f, int lane) {
     if constexpr (KC) {
-        const int r = lane & 15, s = kk * 4 + (lane >> 4);
-        return *reinterpret_cast<const s16x8 *>(tile + (row0 + r) * kBK + ((s ^ (r & 7)) * 8) +
+        const int r = lane & 15, s = lane >> 4;
+        return *reinterpret_cast<const s16x8 *>(tile + (row0 + r) * kBK + ((s ^ (r >> 1 & 3)) * 8) +
                                                 f * 16 * kBK);
     } else {
         const int t = lane & 15, c = (lane >> 4) * 8 + (t >> 2);
@@ -289,7 +294,7 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int f,
         for (int h = 0; h < 2; ++h) {
             constexpr int per_row = ROWS + ROWS * kSkip<KC, ROWS> / 512;
             const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds4 *)(tile + at + (f & ~F) * 16 + (kk * 32 + h * 4) * per_row));
+                (lds4 *)(tile + at + (f & ~F) * 16 + h * 4 * per_row));
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[h * 4 + e] = x[e];
         }
@@ -310,16 +315,28 @@ __device__ __forceinline__ void tile_of(const Args &a, int &ti, int &tj) {
     tj = in / high;
 }
 
+// The main loop, a step (32 of the contraction) at a time:
+//   read:     start the copies of the step three ahead, read this step's
+//             operands into registers, wait for both of these reads and for
+//             the copies of the next step, barrier;
+//   multiply: FI x FJ matrix instructions a wave.
+// A slot is copied into only after the barrier behind its last read.
+//
+// Workgroups of eight waves (PAIRED) run as two groups of four, one wave of
+// each on every SIMD, half a step apart: while one group multiplies the other
+// reads, so that shared memory (a step's reads and copies take as long as its
+// products) and matrix units are busy together.  A barrier behind either half
+// keeps the groups alternating.  Workgroups of four waves share a CU with
+// another workgroup instead.
 template <int OP, class T, int BI, int BJ, int WI, int WJ, bool DIRECT>
 __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     constexpr bool PKC = OP != WGRAD, QKC = OP == FWD;
     constexpr int THREADS = WI * WJ * kWave;
     constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
+    constexpr bool PAIRED = WI * WJ == 8;
+    constexpr int SLOT = kTile<PKC, BI> + kTile<QKC, BJ>;
     static_assert(FJ % 2 == 0, "mask draws pair two 16-column blocks");
-    __shared__ __attribute__((aligned(1024))) uint16_t p0[kTile<PKC, BI>];
-    __shared__ __attribute__((aligned(1024))) uint16_t p1[kTile<PKC, BI>];
-    __shared__ __attribute__((aligned(1024))) uint16_t q0[kTile<QKC, BJ>];
-    __shared__ __attribute__((aligned(1024))) uint16_t q1[kTile<QKC, BJ>];
+    __shared__ __attribute__((aligned(1024))) uint16_t tiles[kSlots * SLOT];
 
     int ti, tj;
     tile_of(a, ti, tj);
@@ -343,73 +360,91 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     static_assert(FI <= 16, "a row of the sums for every block");
     const bool with_db = OP == WGRAD && a.e.db != nullptr && tj == 0 && wj == 0;
 
+    // whole steps go straight to shared memory (DIRECT); a last broken one is
+    // staged through registers
+    const int whole = DIRECT ? static_cast<int>((c1 - c0) / kBK) : 0;
     Stage<PKC, BI, THREADS> sp;
     Stage<QKC, BJ, THREADS> sq;
-    auto load = [&](int s) __attribute__((always_inline)) {
-        sp.load(a.p, a.ldp, i0, a.ni, c0 + static_cast<int64_t>(s) * kBK, c1);
-        sq.load(a.q, a.ldq, j0, a.nj, c0 + static_cast<int64_t>(s) * kBK, c1);
-    };
-    auto compute = [&](const uint16_t *tp, const uint16_t *tq) __attribute__((always_inline)) {
-#pragma unroll
-        for (int kk = 0; kk < kBK / 32; ++kk) {
-            s16x8 fp[FI], fq[FJ];
-#pragma unroll
-            for (int t = 0; t < FJ; ++t) fq[t] = fragment<QKC, BJ>(tq, wj, t, kk, lane);
-#pragma unroll
-            for (int f = 0; f < FI; ++f) fp[f] = fragment<PKC, BI>(tp, wi, f, kk, lane);
-#pragma unroll
-            for (int f = 0; f < FI; ++f)
-#pragma unroll
-                for (int t = 0; t < FJ; ++t) acc[f][t] = mfma<T>(fq[t], fp[f], acc[f][t]);
-            if (OP == WGRAD && with_db) {
-#pragma unroll
-                for (int f = 0; f < FI; ++f) {
-                    const short o = (lane & 15) == f ? static_cast<short>(T::down(1.0f)) : short(0);
-                    sums = mfma<T>(s16x8{o, o, o, o, o, o, o, o}, fp[f], sums);
-                }
-            }
-        }
-    };
-    // whole steps go straight to shared memory; a last broken one is staged
-    const int whole = DIRECT ? static_cast<int>((c1 - c0) / kBK) : 0;
     Direct<PKC, BI, THREADS> dp;
     Direct<QKC, BJ, THREADS> dq;
+    constexpr int COPIES = Direct<PKC, BI, THREADS>::N + Direct<QKC, BJ, THREADS>::N;
     if (DIRECT) {
         dp.init(a.p, a.ldp, i0, a.ni, c0);
         dq.init(a.q, a.ldq, j0, a.nj, c0);
     }
-    auto put = [&](uint16_t *np, uint16_t *nq) __attribute__((always_inline)) {
-        sp.store(np);
-        sq.store(nq);
+    const uint32_t lds = static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t *)tiles));
+    auto slot_of = [&](int s) __attribute__((always_inline)) { return (s & (kSlots - 1)) * SLOT; };
+    auto load = [&](int s) __attribute__((always_inline)) {
+        sp.load(a.p, a.ldp, i0, a.ni, c0 + static_cast<int64_t>(s) * kBK, c1);
+        sq.load(a.q, a.ldq, j0, a.nj, c0 + static_cast<int64_t>(s) * kBK, c1);
     };
-    auto fetch = [&](int s, uint16_t *np, uint16_t *nq) __attribute__((always_inline)) {
-        if (s < whole) {
-            dp.issue(np, wave);
-            dq.issue(nq, wave);
-        } else if (s < steps) {
-            load(s);
-            if (DIRECT) put(np, nq);
+    auto put = [&](int s) __attribute__((always_inline)) {
+        sp.store(tiles + slot_of(s));
+        sq.store(tiles + slot_of(s) + kTile<PKC, BI>);
+    };
+    // makes step s's tile, or starts to; staged steps are loaded one call ahead
+    auto fetch = [&](int s) __attribute__((always_inline)) {
+        if (DIRECT) {
+            if (s < whole) {
+                dp.issue(lds + 2 * slot_of(s), wave);
+                dq.issue(lds + 2 * (slot_of(s) + kTile<PKC, BI>), wave);
+            } else if (s < steps) {
+                load(s);
+                put(s);
+            }
+        } else {
+            if (s < steps) put(s);
+            if (s + 1 < steps) load(s + 1);
         }
     };
-    auto sync = [&]() __attribute__((always_inline)) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the direct copies have landed
-        __syncthreads();
+    // this wave's reads are done, and its copies of all steps up to s
+    auto arrive = [&](int s) __attribute__((always_inline)) {
+        if (DIRECT && s + 2 < whole)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"(2 * COPIES) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     };
-    auto step = [&](int s, const uint16_t *tp, const uint16_t *tq, uint16_t *np, uint16_t *nq) __attribute__((always_inline)) {
-        fetch(s + 1, np, nq);
-        compute(tp, tq);
-        if (!DIRECT && s + 1 < steps) put(np, nq);
-        sync();
-    };
-    if (steps > 0) {
-        fetch(0, p0, q0);
-        if (!DIRECT) put(p0, q0);
-        sync();
-        for (int s = 0; s < steps; s += 2) {
-            step(s, p0, q0, p1, q1);
-            if (s + 1 < steps) step(s + 1, p1, q1, p0, q0);
+
+    if (!DIRECT && steps > 0) load(0);
+    fetch(0);
+    fetch(1);
+    fetch(2);
+    arrive(0);
+    if (PAIRED && wave >= 4) __builtin_amdgcn_s_barrier();
+    for (int s = 0; s < steps; ++s) {
+        const uint16_t *tp = tiles + slot_of(s), *tq = tp + kTile<PKC, BI>;
+        fetch(s + 3);
+        s16x8 fp[FI], fq[FJ];
+#pragma unroll
+        for (int t = 0; t < FJ; ++t) fq[t] = fragment<QKC, BJ>(tq, wj, t, lane);
+#pragma unroll
+        for (int f = 0; f < FI; ++f) fp[f] = fragment<PKC, BI>(tp, wi, f, lane);
+        arrive(s + 1);
+        if (PAIRED) __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int f = 0; f < FI; ++f)
+#pragma unroll
+            for (int t = 0; t < FJ; ++t) acc[f][t] = mfma<T>(fq[t], fp[f], acc[f][t]);
+        if (OP == WGRAD && with_db) {
+#pragma unroll
+            for (int f = 0; f < FI; ++f) {
+                const short o = (lane & 15) == f ? static_cast<short>(T::down(1.0f)) : short(0);
+                sums = mfma<T>(s16x8{o, o, o, o, o, o, o, o}, fp[f], sums);
+            }
+        }
+        if (PAIRED) {
+            __builtin_amdgcn_s_setprio(0);
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
+    if (PAIRED && wave < 4) __builtin_amdgcn_s_barrier();
 
     const int g = lane >> 4;
     const int64_t njp = padded4(a.nj);
@@ -494,11 +529,11 @@ Plan plan_for(int64_t ni, int64_t nj, int64_t nc) {
     if (ceil_div(ni, 256) * ceil_div(nj, 256) < kCUs * 3 / 4) p.bi = p.bj = 128;
     if (ni <= 64) p.bi = 64;
     const int64_t tiles = ceil_div(ni, p.bi) * ceil_div(nj, p.bj);
-    const int64_t steps = ceil_div(nc, kBK);
+    const int64_t steps = ceil_div(nc, 2 * kBK);
     int64_t parts = 1;
     if (tiles < kCUs) parts = std::min<int64_t>(2 * kCUs / std::max<int64_t>(tiles, 1), steps / 4);
     parts = std::max<int64_t>(1, std::min<int64_t>(parts, 64));
-    p.chunk = std::max<int64_t>(ceil_div(steps, parts), 1) * kBK;
+    p.chunk = std::max<int64_t>(ceil_div(steps, parts), 1) * 2 * kBK;
     p.parts = static_cast<int>(std::max<int64_t>(1, ceil_div(nc, p.chunk)));
     return p;
 }
