@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "linear_common.h"
 
@@ -26,8 +27,7 @@ using namespace zero_linear_impl;
 using s16x4 = short __attribute__((ext_vector_type(4)));
 using s16x8 = short __attribute__((ext_vector_type(8)));
 
-constexpr int kBK = 32;    // contraction elements of one step
-constexpr int kSlots = 4;  // steps in shared memory
+constexpr int kBK = 64;  // contraction elements of one step
 
 enum Op { FWD = ZERO_LINEAR, DGRAD = ZERO_LINEAR_DGRAD, WGRAD = ZERO_LINEAR_WGRAD };
 
@@ -47,7 +47,7 @@ struct Args {
     const uint16_t *p, *q;
     int64_t ldp, ldq;
     int64_t ni, nj, nc;
-    int64_t chunk;    // contraction elements of a part, a multiple of 2 kBK
+    int64_t chunk;    // contraction elements of a part, a multiple of kBK
     int32_t parts;
     int32_t tiles_i, tiles_j;
     float *partial;   // [parts][ni][njp], then the column sums [parts][ni]
@@ -151,11 +151,11 @@ __device__ __forceinline__ void emit_db(const Epilogue &e, int64_t i, float v) {
 // ---------------------------------------------------------------------------
 // tiles in shared memory, in 16-byte pieces of eight elements
 //
-// Rows of c: [ROWS][32], piece (row, s) at row * 4 + (s ^ (row / 2 & 3)); a
+// Rows of c: [ROWS][64], piece (row, s) at row * 8 + (s ^ (row & 7)); a
 // lane's operand is one piece, eight consecutive c of its row.  The exclusive
 // or spreads the pieces that eight lanes read at once over all banks.
 //
-// Rows of lanes: [32][ROWS], in 32-byte units of 16 lanes.
+// Rows of lanes: [64][ROWS], in 32-byte units of 16 lanes.
 // ds_read_b64_tr_b16 reads four rows of a unit and hands every lane the four
 // c of its own column; two of them make an operand.  The four rows must lie
 // in different banks: unit u of row c is stored at u ^ flip(c), and tiles of
@@ -177,11 +177,11 @@ constexpr int kTile = ROWS * kBK + ROWS * kBK / 512 * kSkip<KC, ROWS>;
 
 template <bool KC, int ROWS>
 __device__ __forceinline__ int piece_row(int pos) {
-    return KC ? pos >> 2 : pos / (ROWS / 8);
+    return KC ? pos >> 3 : pos / (ROWS / 8);
 }
 template <bool KC, int ROWS>
 __device__ __forceinline__ int piece_slot(int pos) {
-    if (KC) return (pos & 3) ^ ((pos >> 3) & 3);
+    if (KC) return (pos & 7) ^ ((pos >> 3) & 7);
     return (pos % (ROWS / 8)) ^ (2 * flip<ROWS>(pos / (ROWS / 8)));
 }
 
@@ -246,16 +246,20 @@ struct Stage {
 template <bool KC, int ROWS, int THREADS>
 struct Direct {
     static constexpr int N = ROWS * kBK / 8 / THREADS;
+    static constexpr int kRows = THREADS * 8 / ROWS;  // rows of lanes per copy
+    static_assert(KC || kRows % 8 == 0, "a lane's unit has the same place in every copy");
     const char *base;       // of the next step
     int64_t stride;         // bytes from step to step
-    uint32_t off[N];
+    int64_t apart;          // bytes from copy to copy (rows of lanes)
+    uint32_t off[KC ? N : 1];
     __device__ __forceinline__ void init(const uint16_t *p, int64_t ld, int64_t r0, int64_t rows,
                                          int64_t c0) {
         base = reinterpret_cast<const char *>(KC ? p + r0 * ld + c0 : p + c0 * ld + r0);
         stride = (KC ? kBK : kBK * ld) * 2;
+        apart = KC ? 0 : kRows * ld * 2;
         const int last = static_cast<int>(min(rows - r0, static_cast<int64_t>(ROWS))) - (KC ? 1 : 8);
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
+        for (int n = 0; n < (KC ? N : 1); ++n) {
             const int pos = n * THREADS + static_cast<int>(threadIdx.x);
             const int row = piece_row<KC, ROWS>(pos), s = piece_slot<KC, ROWS>(pos);
             off[n] = KC ? static_cast<uint32_t>(min(row, last)) * static_cast<uint32_t>(ld * 2) + s * 16
@@ -263,25 +267,24 @@ struct Direct {
                               min(s * 8, last) * 2;
         }
     }
-    // tile: its byte address in shared memory
-    __device__ __forceinline__ void issue(uint32_t tile, int wave) {
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                         :
-                         : "s"(tile + 2 * piece_at<KC, ROWS>(n * THREADS + wave * kWave)),
-                           "v"(off[n]), "s"(base)
-                         : "memory", "m0");
-        base += stride;
+    // copy n of a step; tile: its byte address in shared memory
+    __device__ __forceinline__ void issue(int n, uint32_t tile, int wave) const {
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :
+                     : "s"(tile + 2 * piece_at<KC, ROWS>(n * THREADS + wave * kWave)),
+                       "v"(off[KC ? n : 0]), "s"(base + n * apart)
+                     : "memory", "m0");
     }
+    __device__ __forceinline__ void next() { base += stride; }
 };
 
-// a lane's operand of 16-row block f from row row0 on: its eight consecutive c
+// a lane's operand of 16-row block f from row row0 on: its eight consecutive
+// c of the 32 that start at kk * 32
 template <bool KC, int ROWS>
-__device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int f, int lane) {
+__device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int f, int kk, int lane) {
     if constexpr (KC) {
-        const int r = lane & 15, s = lane >> 4;
-        return *reinterpret_cast<const s16x8 *>(tile + (row0 + r) * kBK + ((s ^ (r >> 1 & 3)) * 8) +
+        const int r = lane & 15, s = kk * 4 + (lane >> 4);
+        return *reinterpret_cast<const s16x8 *>(tile + (row0 + r) * kBK + ((s ^ (r & 7)) * 8) +
                                                 f * 16 * kBK);
     } else {
         const int t = lane & 15, c = (lane >> 4) * 8 + (t >> 2);
@@ -294,7 +297,7 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int f,
         for (int h = 0; h < 2; ++h) {
             constexpr int per_row = ROWS + ROWS * kSkip<KC, ROWS> / 512;
             const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds4 *)(tile + at + (f & ~F) * 16 + h * 4 * per_row));
+                (lds4 *)(tile + at + (f & ~F) * 16 + (kk * 32 + h * 4) * per_row));
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[h * 4 + e] = x[e];
         }
@@ -315,28 +318,25 @@ __device__ __forceinline__ void tile_of(const Args &a, int &ti, int &tj) {
     tj = in / high;
 }
 
-// The main loop, a step (32 of the contraction) at a time:
-//   read:     start the copies of the step three ahead, read this step's
-//             operands into registers, wait for both of these reads and for
-//             the copies of the next step, barrier;
-//   multiply: FI x FJ matrix instructions a wave.
-// A slot is copied into only after the barrier behind its last read.
-//
-// Workgroups of eight waves (PAIRED) run as two groups of four, one wave of
-// each on every SIMD, half a step apart: while one group multiplies the other
-// reads, so that shared memory (a step's reads and copies take as long as its
-// products) and matrix units are busy together.  A barrier behind either half
-// keeps the groups alternating.  Workgroups of four waves share a CU with
-// another workgroup instead.
-template <int OP, class T, int BI, int BJ, int WI, int WJ, bool DIRECT>
+// The main loop goes by steps of 64 of the contraction, held in one of two
+// buffers, each step in two halves of 32 with operands of their own registers:
+//   first half:   multiply the first 32, reading the second 32 meanwhile;
+//   wait for the reads and for the copies of the next step; barrier;
+//   second half:  multiply the second 32, starting the copies of the step
+//                 after next into this step's buffer, which nobody reads any
+//                 more, and reading the first 32 of the next step.
+// Reads, copies and products are dealt out one by one, so that the matrix
+// unit has work from the same wave while a read is under way: a wave has a
+// large block of its own (128 x 128 in the largest tiles: one wave a SIMD,
+// fewest reads a product) and needs no other wave to fill its gaps.
+template <int OP, class T, int BI, int BJ, int WI, int WJ, bool DIRECT, bool DB>
 __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     constexpr bool PKC = OP != WGRAD, QKC = OP == FWD;
     constexpr int THREADS = WI * WJ * kWave;
     constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
-    constexpr bool PAIRED = WI * WJ == 8;
     constexpr int SLOT = kTile<PKC, BI> + kTile<QKC, BJ>;
     static_assert(FJ % 2 == 0, "mask draws pair two 16-column blocks");
-    __shared__ __attribute__((aligned(1024))) uint16_t tiles[kSlots * SLOT];
+    __shared__ __attribute__((aligned(1024))) uint16_t tiles[2 * SLOT];
 
     int ti, tj;
     tile_of(a, ti, tj);
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     // sums of all FI blocks.
     f32x4 sums = {0.f, 0.f, 0.f, 0.f};
     static_assert(FI <= 16, "a row of the sums for every block");
-    const bool with_db = OP == WGRAD && a.e.db != nullptr && tj == 0 && wj == 0;
+    const bool with_db = DB && tj == 0 && wj == 0;
 
     // whole steps go straight to shared memory (DIRECT); a last broken one is
     // staged through registers
@@ -367,14 +367,14 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     Stage<QKC, BJ, THREADS> sq;
     Direct<PKC, BI, THREADS> dp;
     Direct<QKC, BJ, THREADS> dq;
-    constexpr int COPIES = Direct<PKC, BI, THREADS>::N + Direct<QKC, BJ, THREADS>::N;
+    constexpr int NP = Direct<PKC, BI, THREADS>::N, NQ = Direct<QKC, BJ, THREADS>::N;
     if (DIRECT) {
         dp.init(a.p, a.ldp, i0, a.ni, c0);
         dq.init(a.q, a.ldq, j0, a.nj, c0);
     }
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t *)tiles));
-    auto slot_of = [&](int s) __attribute__((always_inline)) { return (s & (kSlots - 1)) * SLOT; };
+    auto slot_of = [&](int s) __attribute__((always_inline)) { return (s & 1) * SLOT; };
     auto load = [&](int s) __attribute__((always_inline)) {
         sp.load(a.p, a.ldp, i0, a.ni, c0 + static_cast<int64_t>(s) * kBK, c1);
         sq.load(a.q, a.ldq, j0, a.nj, c0 + static_cast<int64_t>(s) * kBK, c1);
@@ -383,68 +383,123 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
         sp.store(tiles + slot_of(s));
         sq.store(tiles + slot_of(s) + kTile<PKC, BI>);
     };
-    // makes step s's tile, or starts to; staged steps are loaded one call ahead
-    auto fetch = [&](int s) __attribute__((always_inline)) {
-        if (DIRECT) {
-            if (s < whole) {
-                dp.issue(lds + 2 * slot_of(s), wave);
-                dq.issue(lds + 2 * (slot_of(s) + kTile<PKC, BI>), wave);
-            } else if (s < steps) {
-                load(s);
-                put(s);
+    auto copy = [&](int n, int s) __attribute__((always_inline)) {
+        if (n < NP)
+            dp.issue(n, lds + 2 * slot_of(s), wave);
+        else if (n < NP + NQ)
+            dq.issue(n - NP, lds + 2 * (slot_of(s) + kTile<PKC, BI>), wave);
+    };
+    auto copied = [&]() __attribute__((always_inline)) {
+        dp.next();
+        dq.next();
+    };
+    s16x8 fp[2][FI], fq[2][FJ];
+    auto read = [&](int n, int s, int kk) __attribute__((always_inline)) {
+        const uint16_t *tp = tiles + slot_of(s), *tq = tp + kTile<PKC, BI>;
+        if (n < FJ)
+            fq[kk][n] = fragment<QKC, BJ>(tq, wj, n, kk, lane);
+        else if (n < FJ + FI)
+            fp[kk][n - FJ] = fragment<PKC, BI>(tp, wi, n - FJ, kk, lane);
+    };
+    // the products of half kk, with reads of half 1 - kk of step rs and (COPY)
+    // copies of step cs between them
+    auto half = [&](auto kk_, auto copy_, int rs, int cs) __attribute__((always_inline)) {
+        constexpr int kk = decltype(kk_)::value, READS = FI + FJ, N = FI * FJ;
+        constexpr bool COPY = decltype(copy_)::value;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            // reads and copies are spread over the first three quarters
+            constexpr int M = N * 3 / 4 > 0 ? N * 3 / 4 : 1;
+            bool placed = false;
+#pragma unroll
+            for (int r = 0; r < READS; ++r)
+                if (r * M / READS == n) {
+                    read(r, rs, 1 - kk);
+                    placed = true;
+                }
+            if (COPY) {
+#pragma unroll
+                for (int c = 0; c < NP + NQ; ++c)
+                    if (c * M / (NP + NQ) == n) {
+                        copy(c, cs);
+                        placed = true;
+                    }
             }
-        } else {
-            if (s < steps) put(s);
-            if (s + 1 < steps) load(s + 1);
+            acc[n / FJ][n % FJ] = mfma<T>(fq[kk][n % FJ], fp[kk][n / FJ], acc[n / FJ][n % FJ]);
+            if (placed) __builtin_amdgcn_sched_barrier(0);
+        }
+        if (DB && with_db) {
+#pragma unroll
+            for (int f = 0; f < FI; ++f) {
+                const short o = (lane & 15) == f ? static_cast<short>(T::down(1.0f)) : short(0);
+                sums = mfma<T>(s16x8{o, o, o, o, o, o, o, o}, fp[kk][f], sums);
+            }
         }
     };
-    // this wave's reads are done, and its copies of all steps up to s
-    auto arrive = [&](int s) __attribute__((always_inline)) {
-        if (DIRECT && s + 2 < whole)
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"(2 * COPIES) : "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    using first = std::integral_constant<int, 0>;
+    using second = std::integral_constant<int, 1>;
+    // this wave's reads are done and what it copied or staged has landed
+    auto arrive = [&]() __attribute__((always_inline)) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    if (!DIRECT && steps > 0) load(0);
-    fetch(0);
-    fetch(1);
-    fetch(2);
-    arrive(0);
-    if (PAIRED && wave >= 4) __builtin_amdgcn_s_barrier();
-    for (int s = 0; s < steps; ++s) {
-        const uint16_t *tp = tiles + slot_of(s), *tq = tp + kTile<PKC, BI>;
-        fetch(s + 3);
-        s16x8 fp[FI], fq[FJ];
+    if constexpr (DIRECT) {
+        if (whole > 0) {
 #pragma unroll
-        for (int t = 0; t < FJ; ++t) fq[t] = fragment<QKC, BJ>(tq, wj, t, lane);
+            for (int n = 0; n < NP + NQ; ++n) copy(n, 0);
+            copied();
+            arrive();
+            if (whole > 1) {
 #pragma unroll
-        for (int f = 0; f < FI; ++f) fp[f] = fragment<PKC, BI>(tp, wi, f, lane);
-        arrive(s + 1);
-        if (PAIRED) __builtin_amdgcn_s_setprio(1);
+                for (int n = 0; n < NP + NQ; ++n) copy(n, 1);
+                copied();
+            }
 #pragma unroll
-        for (int f = 0; f < FI; ++f)
-#pragma unroll
-            for (int t = 0; t < FJ; ++t) acc[f][t] = mfma<T>(fq[t], fp[f], acc[f][t]);
-        if (OP == WGRAD && with_db) {
-#pragma unroll
-            for (int f = 0; f < FI; ++f) {
-                const short o = (lane & 15) == f ? static_cast<short>(T::down(1.0f)) : short(0);
-                sums = mfma<T>(s16x8{o, o, o, o, o, o, o, o}, fp[f], sums);
+            for (int n = 0; n < FI + FJ; ++n) read(n, 0, 0);
+            int s = 0;
+#pragma unroll 1
+            for (; s < whole - 2; ++s) {
+                half(first{}, std::false_type{}, s, 0);
+                arrive();
+                half(second{}, std::true_type{}, s + 1, s + 2);
+                copied();
+            }
+#pragma unroll 1
+            for (; s < whole; ++s) {
+                half(first{}, std::false_type{}, s, 0);
+                arrive();
+                half(second{}, std::false_type{}, s + 1, 0);
             }
         }
-        if (PAIRED) {
-            __builtin_amdgcn_s_setprio(0);
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
+        if (whole < steps) {  // the broken step, in the buffer nobody reads
+            load(whole);
+            put(whole);
+            arrive();
+#pragma unroll
+            for (int n = 0; n < FI + FJ; ++n) read(n, whole, 0);
+            half(first{}, std::false_type{}, whole, 0);
+            half(second{}, std::false_type{}, whole, 0);
+        }
+    } else if (steps > 0) {
+        load(0);
+        put(0);
+        arrive();
+        if (steps > 1) load(1);
+#pragma unroll
+        for (int n = 0; n < FI + FJ; ++n) read(n, 0, 0);
+#pragma unroll 1
+        for (int s = 0; s < steps; ++s) {
+            if (s + 1 < steps) put(s + 1);
+            half(first{}, std::false_type{}, s, 0);
+            arrive();
+            if (s + 2 < steps) load(s + 2);
+            half(second{}, std::false_type{}, s + 1, 0);
         }
     }
-    if (PAIRED && wave < 4) __builtin_amdgcn_s_barrier();
 
     const int g = lane >> 4;
     const int64_t njp = padded4(a.nj);
@@ -472,14 +527,14 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
                 const int64_t j = j0 + wj + t * 16 + g * 4;
                 if (j < a.nj) *reinterpret_cast<f32x4 *>(row + j) = v[t];
             }
-            if (OP == WGRAD && with_db && g == f >> 2)
+            if (DB && with_db && g == f >> 2)
                 a.partial[a.parts * a.ni * njp + part * a.ni + i] = sum_of(f);
             continue;
         }
 #pragma unroll
         for (int t = 0; t < FJ; t += 2)
             emit_pair<OP, T>(a.e, i, j0 + wj + t * 16 + g * 4, a.nj, stream, v[t], v[t + 1]);
-        if (OP == WGRAD && with_db && g == f >> 2) emit_db<T>(a.e, i, sum_of(f));
+        if (DB && with_db && g == f >> 2) emit_db<T>(a.e, i, sum_of(f));
     }
 }
 
@@ -529,11 +584,11 @@ Plan plan_for(int64_t ni, int64_t nj, int64_t nc) {
     if (ceil_div(ni, 256) * ceil_div(nj, 256) < kCUs * 3 / 4) p.bi = p.bj = 128;
     if (ni <= 64) p.bi = 64;
     const int64_t tiles = ceil_div(ni, p.bi) * ceil_div(nj, p.bj);
-    const int64_t steps = ceil_div(nc, 2 * kBK);
+    const int64_t steps = ceil_div(nc, kBK);
     int64_t parts = 1;
     if (tiles < kCUs) parts = std::min<int64_t>(2 * kCUs / std::max<int64_t>(tiles, 1), steps / 4);
     parts = std::max<int64_t>(1, std::min<int64_t>(parts, 64));
-    p.chunk = std::max<int64_t>(ceil_div(steps, parts), 1) * 2 * kBK;
+    p.chunk = std::max<int64_t>(ceil_div(steps, parts), 1) * kBK;
     p.parts = static_cast<int>(std::max<int64_t>(1, ceil_div(nc, p.chunk)));
     return p;
 }
@@ -556,7 +611,11 @@ zero_status run_tiles(Args &a, hipStream_t st) {
     const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j;
     if (tiles > 0x7FFFFFFF) return ZERO_EINVAL;
     const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(a.parts));
-    tile_kernel<OP, T, BI, BJ, WI, WJ, DIRECT><<<grid, WI * WJ * kWave, 0, st>>>(a);
+    // the bias gradient's sums take registers: only where they are asked for
+    if (OP == WGRAD && a.e.db != nullptr)
+        tile_kernel<OP, T, BI, BJ, WI, WJ, DIRECT, OP == WGRAD><<<grid, WI * WJ * kWave, 0, st>>>(a);
+    else
+        tile_kernel<OP, T, BI, BJ, WI, WJ, DIRECT, false><<<grid, WI * WJ * kWave, 0, st>>>(a);
     return launch_status();
 }
 
