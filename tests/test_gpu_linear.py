@@ -56,7 +56,8 @@ def product64(a, b):
 SIZES = [(1, 1, 1), (1, 64, 64), (1, 6400, 1600), (3, 5, 7), (2, 130, 63), (16, 48, 4096),
          (17, 33, 65), (64, 128, 64), (65, 129, 127), (128, 128, 128), (127, 255, 129),
          (100, 1, 300), (5, 300, 0), (256, 256, 64), (300, 700, 513), (31, 40, 8191),
-         (4100, 2300, 72), (3333, 3001, 130), (9, 40000, 24)]
+         (4100, 2300, 72), (3333, 3001, 130), (9, 40000, 24), (4200, 4176, 72),
+         (4200, 72, 4176), (72, 4200, 4176), (24, 100, 1300), (32, 2000, 200), (33, 90, 1000)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])

@@ -89,7 +89,7 @@ def status(op, **change):
     return fn(*{**base, **change}.values())
 
 
-LONG = dict(m=8, n=8, k=1 << 16)   # a divided contraction for linear
+LONG = dict(m=40, n=8, k=1 << 16)   # a divided contraction for linear
 
 
 @cpu_only

@@ -22,7 +22,6 @@ ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH, ZERO_ACT_SILU =
 ZERO_LINEAR, ZERO_LINEAR_DGRAD, ZERO_LINEAR_WGRAD = range(3)
 
 _CODE = {torch.bfloat16: ZERO_BF16, torch.float16: ZERO_FP16, torch.float32: ZERO_FP32}
-_WIDTH = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4}
 
 
 class _DropoutParams(ctypes.Structure):
@@ -44,6 +43,7 @@ class ZeroDropout:
     def _c(self, device):
         return _DropoutParams(self.p, self.seed & 0xFFFFFFFFFFFFFFFF,
                               self.offset & 0xFFFFFFFFFFFFFFFF, self.row0,
+                              None if self.step is None else
                               _buf(self.step, "drop.step", 1, torch.int64, device))
 
 
@@ -68,34 +68,43 @@ def _declare(L):
 _declare(_lib)
 
 
-def _mat(t, what: str, rows=None, cols=None, dtype=None, device=None):
-    """(address, row stride) of a GPU matrix with contiguous rows, its shape,
-    type and device as given (None: whatever they are)."""
-    if not getattr(t, "is_cuda", False):
+def _mat(t, what, shape, dtype, dev):
+    """(address, row stride) of a GPU matrix of this shape and type on device
+    number dev, with contiguous rows."""
+    if t.is_cuda and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        s0, s1 = t.stride()
+        if s1 == 1 and s0 >= shape[1]:
+            return t.data_ptr(), s0
+    return _odd_mat(t, what, shape, dtype, dev)
+
+
+def _odd_mat(t, what, shape, dtype, dev):
+    """_mat for single rows and columns, whose strides mean nothing; else the refusal."""
+    if not t.is_cuda:
         raise TypeError(f"{what}: a GPU tensor is required")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {dtype} expected, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, the call's tensors are on cuda:{dev}")
     if t.dim() != 2:
         raise TypeError(f"{what}: a 2-D tensor is required, got {t.dim()}-D")
-    if dtype is None:
-        if t.dtype not in _CODE:
-            raise TypeError(f"{what}: bfloat16, float16 or float32 expected, got {t.dtype}")
-    elif t.dtype != dtype:
-        raise TypeError(f"{what}: {dtype} expected, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what}: on {t.device}, the call's tensors are on {device}")
-    r, c = t.shape
-    if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{what}: [{rows if rows is not None else 'any'}]"
-                         f"[{cols if cols is not None else 'any'}] expected, got [{r}][{c}]")
-    s0, s1 = t.stride()
-    if s1 != 1 and c > 1:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: {tuple(shape)} expected, got {tuple(t.shape)}")
+    (r, c), (s0, s1) = t.shape, t.stride()
+    if c > 1 and s1 != 1:
         raise TypeError(f"{what}: rows of contiguous elements are required")
     if r > 1 and s0 < c:
         raise TypeError(f"{what}: rows that do not overlap are required (row stride {s0})")
     return t.data_ptr(), (s0 if r > 1 else max(c, 1))
 
 
-def _optional(t, what, rows, cols, dtype, device):
-    return (None, cols) if t is None else _mat(t, what, rows, cols, dtype, device)
+def _shape(t, what):
+    """a matrix argument's own shape and device number"""
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{what}: a GPU tensor is required")
+    if t.dim() != 2:
+        raise TypeError(f"{what}: a 2-D tensor is required, got {t.dim()}-D")
+    return t.shape
 
 
 def _out_type(t, dt, what):
@@ -124,26 +133,31 @@ def _scratch(op, m, n, k, workspace, stream, device):
     """(address, bytes) of the product's workspace: the caller's, or a new
     one allocated on the call's stream (so that freeing it on return is
     ordered after the kernels)."""
-    need = _lib.zero_linear_workspace_bytes(op, m, n, k)
-    if need <= 0:
-        return None, 0
     if workspace is None:
+        need = _lib.zero_linear_workspace_bytes(op, m, n, k)
+        if need <= 0:
+            return None, 0
         with torch.cuda.stream(_torch_stream(stream, device)):
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return workspace.data_ptr(), need
-    have = workspace.numel() * workspace.element_size()
-    if have < need:
-        raise ValueError(f"workspace: {need} bytes needed, the tensor holds {have}")
-    return _buf(workspace, "workspace", 0, device=device), have
+    return _buf(workspace, "workspace", 0, device=device).value, \
+        workspace.numel() * workspace.element_size()
 
 
-def _call(fn, what, device, stream, *args):
-    s = _torch_stream(stream, device).cuda_stream
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            _check(fn(*args, s), what)
+def _call(fn, what, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device current; None is that
+    device's current stream."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, stream)
     else:
-        _check(fn(*args, s), what)
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status:
+        _check(status, what)
 
 
 def zero_linear(x, w, y, bias=None, act: int = ZERO_ACT_NONE, drop=None, residual=None, z=None,
@@ -153,19 +167,20 @@ def zero_linear(x, w, y, bias=None, act: int = ZERO_ACT_NONE, drop=None, residua
     itself), z (optional) [m][n] of x's type.  drop: a ZeroDropout or None.
     A workspace tensor is allocated where one is needed unless one of
     zero_linear_workspace_bytes(ZERO_LINEAR, m, n, k) bytes is passed."""
-    dt, d = _in_type(x, "x"), x.device
-    px, ldx = _mat(x, "x", dtype=dt)
-    m, k = x.shape
-    pw, ldw = _mat(w, "w", None, k, dt, d)
-    n = w.shape[0]
-    py, ldy = _mat(y, "y", m, n, _out_type(y, dt, "y"), d)
-    pr, ldr = _optional(residual, "residual", m, n, y.dtype, d)
-    pz, ldz = _optional(z, "z", m, n, dt, d)
-    ws, nb = _scratch(ZERO_LINEAR, m, n, k, workspace, stream, d)
-    _call(_lib.zero_linear, "zero_linear", d, stream, px, _CODE[dt], ldx, pw, ldw,
-          _buf(bias, "bias", n, dt, d), m, n, k, act,
-          None if drop is None else ctypes.byref(drop._c(d)), pr, ldr, py, _CODE[y.dtype], ldy,
-          pz, ldz, ws, nb)
+    dt = _in_type(x, "x")
+    m, k = _shape(x, "x")
+    n = _shape(w, "w")[0]
+    dev, out, yt = x.get_device(), (m, n), _out_type(y, dt, "y")
+    px, ldx = _mat(x, "x", (m, k), dt, dev)
+    pw, ldw = _mat(w, "w", (n, k), dt, dev)
+    py, ldy = _mat(y, "y", out, yt, dev)
+    pr, ldr = (None, n) if residual is None else _mat(residual, "residual", out, yt, dev)
+    pz, ldz = (None, n) if z is None else _mat(z, "z", out, dt, dev)
+    ws, nb = _scratch(ZERO_LINEAR, m, n, k, workspace, stream, x.device)
+    _call(_lib.zero_linear, "zero_linear", dev, stream, px, _CODE[dt], ldx, pw, ldw,
+          None if bias is None else _buf(bias, "bias", n, dt, x.device), m, n, k, act,
+          None if drop is None else drop._c(x.device), pr, ldr, py, _CODE[yt], ldy, pz, ldz, ws,
+          nb)
 
 
 def zero_linear_dgrad(dy, w, dx, act: int = ZERO_ACT_NONE, z=None, drop=None, residual=None,
@@ -174,18 +189,19 @@ def zero_linear_dgrad(dy, w, dx, act: int = ZERO_ACT_NONE, z=None, drop=None, re
     fp16, dx [m][k] of that type or fp32, residual of dx's type (it may be dx
     itself).  act, z [m][k] and drop are those of the call that made this
     layer's input.  Workspace as for zero_linear."""
-    dt, d = _in_type(dy, "dy"), dy.device
-    py, lddy = _mat(dy, "dy", dtype=dt)
-    m, n = dy.shape
-    pw, ldw = _mat(w, "w", n, None, dt, d)
-    k = w.shape[1]
-    px, lddx = _mat(dx, "dx", m, k, _out_type(dx, dt, "dx"), d)
-    pr, ldr = _optional(residual, "residual", m, k, dx.dtype, d)
-    pz, ldz = _optional(z, "z", m, k, dt, d)
-    ws, nb = _scratch(ZERO_LINEAR_DGRAD, m, n, k, workspace, stream, d)
-    _call(_lib.zero_linear_dgrad, "zero_linear_dgrad", d, stream, py, _CODE[dt], lddy, pw, ldw, m,
-          n, k, act, pz, ldz, None if drop is None else ctypes.byref(drop._c(d)), pr, ldr, px,
-          _CODE[dx.dtype], lddx, ws, nb)
+    dt = _in_type(dy, "dy")
+    m, n = _shape(dy, "dy")
+    k = _shape(w, "w")[1]
+    dev, out, xt = dy.get_device(), (m, k), _out_type(dx, dt, "dx")
+    py, lddy = _mat(dy, "dy", (m, n), dt, dev)
+    pw, ldw = _mat(w, "w", (n, k), dt, dev)
+    px, lddx = _mat(dx, "dx", out, xt, dev)
+    pr, ldr = (None, k) if residual is None else _mat(residual, "residual", out, xt, dev)
+    pz, ldz = (None, k) if z is None else _mat(z, "z", out, dt, dev)
+    ws, nb = _scratch(ZERO_LINEAR_DGRAD, m, n, k, workspace, stream, dy.device)
+    _call(_lib.zero_linear_dgrad, "zero_linear_dgrad", dev, stream, py, _CODE[dt], lddy, pw, ldw,
+          m, n, k, act, pz, ldz, None if drop is None else drop._c(dy.device), pr, ldr, px,
+          _CODE[xt], lddx, ws, nb)
 
 
 def zero_linear_wgrad(dy, x, dw, db=None, accumulate: bool = False, stream=None, workspace=None):
@@ -193,26 +209,31 @@ def zero_linear_wgrad(dy, x, dw, db=None, accumulate: bool = False, stream=None,
     [m][k] bf16 or fp16, dw [n][k] and db (n elements) of that type or fp32,
     usually places in a flat gradient row; accumulate adds to what they hold
     (a later micro-batch).  Workspace as for zero_linear."""
-    dt, d = _in_type(dy, "dy"), dy.device
-    py, lddy = _mat(dy, "dy", dtype=dt)
-    m, n = dy.shape
-    px, ldx = _mat(x, "x", m, None, dt, d)
-    k = x.shape[1]
-    pg, lddw = _mat(dw, "dw", n, k, _out_type(dw, dt, "dw"), d)
-    ws, nb = _scratch(ZERO_LINEAR_WGRAD, m, n, k, workspace, stream, d)
-    _call(_lib.zero_linear_wgrad, "zero_linear_wgrad", d, stream, py, _CODE[dt], lddy, px, ldx, m,
-          n, k, pg, _CODE[dw.dtype], lddw, _buf(db, "db", n, dw.dtype, d), int(bool(accumulate)),
-          ws, nb)
+    dt = _in_type(dy, "dy")
+    m, n = _shape(dy, "dy")
+    k = _shape(x, "x")[1]
+    dev, gt = dy.get_device(), _out_type(dw, dt, "dw")
+    py, lddy = _mat(dy, "dy", (m, n), dt, dev)
+    px, ldx = _mat(x, "x", (m, k), dt, dev)
+    pg, lddw = _mat(dw, "dw", (n, k), gt, dev)
+    ws, nb = _scratch(ZERO_LINEAR_WGRAD, m, n, k, workspace, stream, dy.device)
+    _call(_lib.zero_linear_wgrad, "zero_linear_wgrad", dev, stream, py, _CODE[dt], lddy, px, ldx,
+          m, n, k, pg, _CODE[gt], lddw,
+          None if db is None else _buf(db, "db", n, gt, dy.device), int(bool(accumulate)), ws, nb)
 
 
 def zero_dropout(x, y, drop, residual=None, stream=None):
     """y = residual + D(x) (2-D, bf16, fp16 or fp32; y may be x or residual
     itself).  The backward pass is the same call on the gradient."""
-    px, ldx = _mat(x, "x")
-    d, (m, n) = x.device, x.shape
-    py, ldy = _mat(y, "y", m, n, x.dtype, d)
-    pr, ldr = _optional(residual, "residual", m, n, x.dtype, d)
+    shape, dt = _shape(x, "x"), x.dtype
+    code = _CODE.get(dt)
+    if code is None:
+        raise TypeError(f"x: bfloat16, float16 or float32 expected, got {dt}")
     if drop is None:
         raise TypeError("drop: a ZeroDropout is required")
-    _call(_lib.zero_dropout, "zero_dropout", d, stream, px, _CODE[x.dtype], ldx, m, n,
-          ctypes.byref(drop._c(d)), pr, ldr, py, ldy)
+    dev = x.get_device()
+    px, ldx = _mat(x, "x", shape, dt, dev)
+    py, ldy = _mat(y, "y", shape, dt, dev)
+    pr, ldr = (None, shape[1]) if residual is None else _mat(residual, "residual", shape, dt, dev)
+    _call(_lib.zero_dropout, "zero_dropout", dev, stream, px, code, ldx, shape[0], shape[1],
+          drop._c(x.device), pr, ldr, py, ldy)

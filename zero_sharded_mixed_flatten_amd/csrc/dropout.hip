@@ -21,7 +21,6 @@ struct Args {
     void *y;
     int64_t ldx, ldr, ldy;
     int64_t rows, cols;
-    int32_t vec;
     Drop drop;
 };
 
@@ -29,20 +28,20 @@ struct FP32 {};
 
 template <class T>
 struct Access {
-    static __device__ __forceinline__ f32x4 load(const void *p, int64_t at, int n, bool vec) {
-        return load16<T>(static_cast<const uint16_t *>(p) + at, n, vec);
+    static __device__ __forceinline__ f32x4 load(const void *p, int64_t at, int n) {
+        return load16<T>(static_cast<const uint16_t *>(p) + at, n);
     }
-    static __device__ __forceinline__ void store(void *p, int64_t at, f32x4 v, int n, bool vec) {
-        store16<T>(static_cast<uint16_t *>(p) + at, v, n, vec);
+    static __device__ __forceinline__ void store(void *p, int64_t at, f32x4 v, int n) {
+        store16<T>(static_cast<uint16_t *>(p) + at, v, n);
     }
 };
 template <>
 struct Access<FP32> {
-    static __device__ __forceinline__ f32x4 load(const void *p, int64_t at, int n, bool vec) {
-        return load32(static_cast<const float *>(p) + at, n, vec);
+    static __device__ __forceinline__ f32x4 load(const void *p, int64_t at, int n) {
+        return load32(static_cast<const float *>(p) + at, n);
     }
-    static __device__ __forceinline__ void store(void *p, int64_t at, f32x4 v, int n, bool vec) {
-        store32(static_cast<float *>(p) + at, v, n, vec);
+    static __device__ __forceinline__ void store(void *p, int64_t at, f32x4 v, int n) {
+        store32(static_cast<float *>(p) + at, v, n);
     }
 };
 
@@ -55,16 +54,15 @@ __global__ void __launch_bounds__(256) dropout_kernel(Args a) {
     const int64_t i = id / quads, u = id - i * quads;
     const int64_t j = u / 4 * 32 + u % 4 * 4;
     if (j >= a.cols) return;
-    const bool vec = a.vec != 0;
     const int n0 = static_cast<int>(a.cols - j < 4 ? a.cols - j : 4);
     const int64_t left = a.cols - j - 16;
     const int n1 = static_cast<int>(left < 0 ? 0 : left < 4 ? left : 4);
-    f32x4 v0 = A::load(a.x, i * a.ldx + j, n0, vec);
-    f32x4 v1 = A::load(a.x, i * a.ldx + j + 16, n1, vec);
+    f32x4 v0 = A::load(a.x, i * a.ldx + j, n0);
+    f32x4 v1 = A::load(a.x, i * a.ldx + j + 16, n1);
     f32x4 r0 = {0.f, 0.f, 0.f, 0.f}, r1 = r0;
     if (a.res != nullptr) {
-        r0 = A::load(a.res, i * a.ldr + j, n0, vec);
-        r1 = A::load(a.res, i * a.ldr + j + 16, n1, vec);
+        r0 = A::load(a.res, i * a.ldr + j, n0);
+        r1 = A::load(a.res, i * a.ldr + j + 16, n1);
     }
     if (a.drop.on) {
         const u32x4 w = drop_words(a.drop, drop_stream(a.drop), static_cast<uint32_t>(i),
@@ -76,14 +74,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(Args a) {
         v0 = r0 + v0;
         v1 = r1 + v1;
     }
-    A::store(a.y, i * a.ldy + j, v0, n0, vec);
-    A::store(a.y, i * a.ldy + j + 16, v1, n1, vec);
-}
-
-bool quads_aligned(const Mat &m) {
-    return m.p == nullptr ||
-           (reinterpret_cast<uintptr_t>(m.p) % static_cast<uintptr_t>(4 * m.elem) == 0 &&
-            (m.rows <= 1 || m.ld % 4 == 0));
+    A::store(a.y, i * a.ldy + j, v0, n0);
+    A::store(a.y, i * a.ldy + j + 16, v1, n1);
 }
 
 }  // namespace
@@ -115,7 +107,6 @@ extern "C" zero_status zero_dropout(const void *x, zero_dtype dt, int64_t ldx, i
     a.ldy = ldy;
     a.rows = rows;
     a.cols = cols;
-    a.vec = quads_aligned(mx) && quads_aligned(mr) && quads_aligned(my);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const int64_t quads = (cols + 31) / 32 * 4;
     const int64_t blocks = (rows * quads + 255) / 256;

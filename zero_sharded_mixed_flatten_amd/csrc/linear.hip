@@ -39,7 +39,6 @@ struct Epilogue {
     void *db;         // wgrad
     int64_t ldr, ldo, ldz;
     int32_t act, out_f32, accumulate;
-    int32_t vec;      // every row of out, res, z and bias is aligned for four elements
     Drop drop;
 };
 
@@ -50,6 +49,7 @@ struct Args {
     int64_t chunk;    // contraction elements of a part, a multiple of kBK
     int32_t parts;
     int32_t tiles_i, tiles_j;
+    int32_t quarter;  // >= 0: the workgroups are quarters of the tiles from here on
     float *partial;   // [parts][ni][njp], then the column sums [parts][ni]
     Epilogue e;
 };
@@ -80,28 +80,27 @@ __device__ __forceinline__ f32x4 mfma<FP16>(s16x8 a, s16x8 b, f32x4 c) {
 template <int OP, class T>
 __device__ __forceinline__ void emit(const Epilogue &e, int64_t i, int64_t j, int n, f32x4 v,
                                      u32x4 words, int half) {
-    const bool vec = e.vec != 0;
     if constexpr (OP == WGRAD) {
         if (e.out_f32) {
             float *o = static_cast<float *>(e.out) + i * e.ldo + j;
-            if (e.accumulate) v = load32(o, n, vec) + v;
-            store32(o, v, n, vec);
+            if (e.accumulate) v = load32(o, n) + v;
+            store32(o, v, n);
         } else {
             uint16_t *o = static_cast<uint16_t *>(e.out) + i * e.ldo + j;
-            if (e.accumulate) v = load16<T>(o, n, vec) + v;
-            store16<T>(o, v, n, vec);
+            if (e.accumulate) v = load16<T>(o, n) + v;
+            store16<T>(o, v, n);
         }
         return;
     }
     if constexpr (OP == FWD) {
-        if (e.bias != nullptr) v += load16<T>(e.bias + j, n, vec);
-        if (e.z != nullptr) store16<T>(e.z + i * e.ldz + j, v, n, vec);
+        if (e.bias != nullptr) v += load16<T>(e.bias + j, n);
+        if (e.z != nullptr) store16<T>(e.z + i * e.ldz + j, v, n);
         if (e.act != ZERO_ACT_NONE) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = act_value(v[k], e.act);
         }
     } else if (e.act != ZERO_ACT_NONE) {
-        const f32x4 z = load16<T>(e.z + i * e.ldz + j, n, vec);
+        const f32x4 z = load16<T>(e.z + i * e.ldz + j, n);
         if (e.act == ZERO_ACT_RELU) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = z[k] > 0.0f ? v[k] : 0.0f;
@@ -113,12 +112,12 @@ __device__ __forceinline__ void emit(const Epilogue &e, int64_t i, int64_t j, in
     if (e.drop.on) v = drop_apply(e.drop, words, half, v);
     if (e.out_f32) {
         if (e.res != nullptr)
-            v = load32(static_cast<const float *>(e.res) + i * e.ldr + j, n, vec) + v;
-        store32(static_cast<float *>(e.out) + i * e.ldo + j, v, n, vec);
+            v = load32(static_cast<const float *>(e.res) + i * e.ldr + j, n) + v;
+        store32(static_cast<float *>(e.out) + i * e.ldo + j, v, n);
     } else {
         if (e.res != nullptr)
-            v = load16<T>(static_cast<const uint16_t *>(e.res) + i * e.ldr + j, n, vec) + v;
-        store16<T>(static_cast<uint16_t *>(e.out) + i * e.ldo + j, v, n, vec);
+            v = load16<T>(static_cast<const uint16_t *>(e.res) + i * e.ldr + j, n) + v;
+        store16<T>(static_cast<uint16_t *>(e.out) + i * e.ldo + j, v, n);
     }
 }
 
@@ -308,8 +307,8 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int f,
 // The tile of this workgroup.  Workgroups go round the 8 XCDs in turn; each
 // XCD is given one contiguous run of tiles, taken in bands of 8 rows of
 // tiles, so that the tiles at work in one L2 share their operands.
-__device__ __forceinline__ void tile_of(const Args &a, int &ti, int &tj) {
-    const int total = a.tiles_i * a.tiles_j, b = static_cast<int>(blockIdx.x);
+__device__ __forceinline__ void tile_of(const Args &a, int b, int &ti, int &tj) {
+    const int total = a.tiles_i * a.tiles_j;
     const int x = b & 7, q = total >> 3, r = total & 7;
     const int id = x * q + (x < r ? x : r) + (b >> 3);
     const int band = 8 * a.tiles_j, first = id / band * 8;
@@ -339,7 +338,14 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     __shared__ __attribute__((aligned(1024))) uint16_t tiles[2 * SLOT];
 
     int ti, tj;
-    tile_of(a, ti, tj);
+    if (BI == 128 && a.quarter >= 0) {
+        tile_of(a, a.quarter + static_cast<int>(blockIdx.x >> 2), ti, tj);
+        ti = 2 * ti + (blockIdx.x >> 1 & 1);
+        tj = 2 * tj + (blockIdx.x & 1);
+        if (static_cast<int64_t>(ti) * BI >= a.ni || static_cast<int64_t>(tj) * BJ >= a.nj) return;
+    } else {
+        tile_of(a, static_cast<int>(blockIdx.x), ti, tj);
+    }
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     const int wi = wave / WJ * (BI / WI), wj = wave % WJ * (BJ / WJ);
@@ -538,6 +544,85 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     }
 }
 
+// Few rows of x (decoding): the weight's bytes are all that counts.  A
+// workgroup has 16 columns of the output, so that there is one for every CU
+// at the usual widths; its eight waves take chunks of 128 of the contraction
+// in turn, straight from global memory into the operand registers (a lane's
+// operand is 16 contiguous bytes of a row of W), the next chunk's loads under
+// way while one is multiplied.  The waves' sums are added in their order in
+// shared memory: one launch, no workspace.  Rows past the last repeat it;
+// their outputs are not stored.
+constexpr int kSkinnyWaves = 8, kSkinnyChunk = 128;
+
+template <class T, int R>
+__global__ void __launch_bounds__(kSkinnyWaves *kWave) skinny_kernel(Args a) {
+    constexpr int U = kSkinnyChunk / 32;
+    __shared__ f32x4 part[kSkinnyWaves][R][kWave];
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const uint16_t *qp = a.q + min(j0 + r, a.nj - 1) * a.ldq + g * 8;
+    const uint16_t *pp[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        pp[i] = a.p + min(static_cast<int64_t>(i * 16 + r), a.ni - 1) * a.ldp + g * 8;
+    f32x4 acc[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Chunk {
+        u32x4 q[U], p[R][U];
+    };
+    auto load = [&](Chunk &c, int64_t at, auto whole) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t n = decltype(whole)::value ? 8 : a.nc - (at + u * 32 + g * 8);
+            c.q[u] = load_piece(qp + at + u * 32, n);
+#pragma unroll
+            for (int i = 0; i < R; ++i) c.p[i][u] = load_piece(pp[i] + at + u * 32, n);
+        }
+    };
+    auto multiply = [&](const Chunk &c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                acc[i] = mfma<T>(__builtin_bit_cast(s16x8, c.q[u]),
+                                 __builtin_bit_cast(s16x8, c.p[i][u]), acc[i]);
+    };
+    const int64_t chunks = a.nc / kSkinnyChunk;
+    int64_t c = wave;
+    Chunk x, y;
+    if (c < chunks) load(x, c * kSkinnyChunk, std::true_type{});
+    while (c < chunks) {
+        c += kSkinnyWaves;
+        if (c < chunks) load(y, c * kSkinnyChunk, std::true_type{});
+        multiply(x);
+        if (c >= chunks) break;
+        c += kSkinnyWaves;
+        if (c < chunks) load(x, c * kSkinnyChunk, std::true_type{});
+        multiply(y);
+    }
+    if (chunks * kSkinnyChunk < a.nc && wave == static_cast<int>(chunks % kSkinnyWaves)) {
+        load(x, chunks * kSkinnyChunk, std::false_type{});
+        multiply(x);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    if (wave >= R) return;
+    const int64_t i = wave * 16 + r, j = j0 + g * 4;
+    if (i >= a.ni || j >= a.nj) return;
+    f32x4 v = part[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kSkinnyWaves; ++w) v += part[w][wave][lane];
+    u32x4 words = {0u, 0u, 0u, 0u};
+    if (a.e.drop.on)
+        words = drop_words(a.e.drop, drop_stream(a.e.drop), static_cast<uint32_t>(i),
+                           static_cast<uint32_t>((j >> 5) * 4 + ((j & 15) >> 2)));
+    emit<FWD, T>(a.e, i, j, static_cast<int>(a.nj - j < 4 ? a.nj - j : 4), v, words,
+                 static_cast<int>(j >> 4) & 1);
+}
+
 // Adds the parts of a divided contraction in their order and finishes the
 // outputs; a thread has the two quads that share a draw of the mask.
 template <int OP, class T>
@@ -573,13 +658,14 @@ __global__ void __launch_bounds__(256) join_kernel(Args a) {
 constexpr int kCUs = 256;
 
 struct Plan {
-    int bi, bj, parts;
+    int bi, bj, parts;  // bi == 16 or 32: the kernel for few rows
     int64_t chunk;
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-Plan plan_for(int64_t ni, int64_t nj, int64_t nc) {
+Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
+    if (op == FWD && ni <= 32) return Plan{ni <= 16 ? 16 : 32, 16, 1, nc};
     Plan p{256, 256, 1, 0};
     if (ceil_div(ni, 256) * ceil_div(nj, 256) < kCUs * 3 / 4) p.bi = p.bj = 128;
     if (ni <= 64) p.bi = 64;
@@ -605,26 +691,49 @@ bool direct_ok(const uint16_t *p, int64_t ld, int64_t lanes) {
 }
 
 template <int OP, class T, int BI, int BJ, int WI, int WJ, bool DIRECT>
-zero_status run_tiles(Args &a, hipStream_t st) {
-    a.tiles_i = static_cast<int32_t>(ceil_div(a.ni, BI));
-    a.tiles_j = static_cast<int32_t>(ceil_div(a.nj, BJ));
-    const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j;
-    if (tiles > 0x7FFFFFFF) return ZERO_EINVAL;
-    const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(a.parts));
+void run_grid(const Args &a, int64_t groups, hipStream_t st) {
+    const dim3 grid(static_cast<uint32_t>(groups), static_cast<uint32_t>(a.parts));
     // the bias gradient's sums take registers: only where they are asked for
     if (OP == WGRAD && a.e.db != nullptr)
         tile_kernel<OP, T, BI, BJ, WI, WJ, DIRECT, OP == WGRAD><<<grid, WI * WJ * kWave, 0, st>>>(a);
     else
         tile_kernel<OP, T, BI, BJ, WI, WJ, DIRECT, false><<<grid, WI * WJ * kWave, 0, st>>>(a);
+}
+
+template <int OP, class T, int BI, int BJ, int WI, int WJ, bool DIRECT>
+zero_status run_tiles(Args &a, hipStream_t st) {
+    a.tiles_i = static_cast<int32_t>(ceil_div(a.ni, BI));
+    a.tiles_j = static_cast<int32_t>(ceil_div(a.nj, BJ));
+    a.quarter = -1;
+    const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j;
+    if (tiles > 0x7FFFFFFF) return ZERO_EINVAL;
+    // One of the largest tiles occupies a CU.  What is left after the last
+    // whole round of them, up to half a round, runs as quarters, two to a CU.
+    const int64_t rest = tiles % kCUs;
+    if (BI == 256 && tiles > kCUs && rest > 0 && rest <= kCUs / 2) {
+        run_grid<OP, T, BI, BJ, WI, WJ, DIRECT>(a, tiles - rest, st);
+        a.quarter = static_cast<int32_t>(tiles - rest);
+        run_grid<OP, T, 128, 128, 2, 2, DIRECT>(a, 4 * rest, st);
+    } else {
+        run_grid<OP, T, BI, BJ, WI, WJ, DIRECT>(a, tiles, st);
+    }
     return launch_status();
 }
 
 template <int OP, class T>
 zero_status launch(Args a, void *stream) {
-    const Plan p = plan_for(a.ni, a.nj, a.nc);
+    const Plan p = plan_for(OP, a.ni, a.nj, a.nc);
     a.chunk = p.chunk;
     a.parts = p.parts;
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (OP == FWD && p.bi <= 32) {
+        const uint32_t groups = static_cast<uint32_t>(ceil_div(a.nj, 16));
+        if (p.bi == 16)
+            skinny_kernel<T, 1><<<groups, kSkinnyWaves * kWave, 0, st>>>(a);
+        else
+            skinny_kernel<T, 2><<<groups, kSkinnyWaves * kWave, 0, st>>>(a);
+        return launch_status();
+    }
     const bool d = direct_ok(a.p, a.ldp, OP == WGRAD ? a.ni : 0) &&
                    direct_ok(a.q, a.ldq, OP == FWD ? 0 : a.nj);
     zero_status status;
@@ -648,13 +757,6 @@ zero_status launch(Args a, void *stream) {
 template <int OP>
 zero_status launch(const Args &a, zero_dtype dt, void *stream) {
     return dt == ZERO_BF16 ? launch<OP, BF16>(a, stream) : launch<OP, FP16>(a, stream);
-}
-
-// every row of a matrix starts at a multiple of four elements
-bool quads(const Mat &m) {
-    return m.empty() || m.p == nullptr ||
-           (reinterpret_cast<uintptr_t>(m.p) % static_cast<uintptr_t>(4 * m.elem) == 0 &&
-            (m.rows <= 1 || m.ld % 4 == 0));
 }
 
 bool workspace_ok(int64_t need, const void *ws, int64_t bytes) {
@@ -685,7 +787,7 @@ zero_status product(const Mat &p, const Mat &q, zero_dtype dt, const Shape &s, c
         return ZERO_EINVAL;
     if (OP == DGRAD && act != ZERO_ACT_NONE && z.p == nullptr && !out.empty()) return ZERO_EINVAL;
     if (out.empty()) return ZERO_OK;
-    const int64_t need = partial_bytes(plan_for(s.ni, s.nj, s.nc), s.ni, s.nj);
+    const int64_t need = partial_bytes(plan_for(OP, s.ni, s.nj, s.nc), s.ni, s.nj);
     if (!workspace_ok(need, workspace, workspace_bytes)) return ZERO_EINVAL;
     const bool z_out = OP == FWD;
     const Span sp = p.span(), sq = q.span(), sb = bias.span(), sr = res.span(), so = out.span(),
@@ -717,7 +819,6 @@ zero_status product(const Mat &p, const Mat &q, zero_dtype dt, const Shape &s, c
     a.e.ldz = z.ld;
     a.e.act = act;
     a.e.out_f32 = out.elem == 4;
-    a.e.vec = quads(out) && quads(res) && quads(z) && quads(bias);
     return launch<OP>(a, dt, stream);
 }
 
@@ -731,7 +832,7 @@ int64_t zero_linear_workspace_bytes(zero_linear_op op, int64_t m, int64_t n, int
         return -1;
     const Shape s = shape_of(op, m, n, k);
     if (s.ni == 0 || s.nj == 0) return 0;
-    return partial_bytes(plan_for(s.ni, s.nj, s.nc), s.ni, s.nj);
+    return partial_bytes(plan_for(op, s.ni, s.nj, s.nc), s.ni, s.nj);
 }
 
 zero_status zero_linear(const void *x, zero_dtype dt, int64_t ldx, const void *w, int64_t ldw,
@@ -780,7 +881,7 @@ zero_status zero_linear_wgrad(const void *dy, zero_dtype dt, int64_t lddy, const
         return ZERO_EINVAL;
     }
     const Shape s = shape_of(WGRAD, m, n, k);
-    const int64_t need = partial_bytes(plan_for(s.ni, s.nj, s.nc), s.ni, s.nj);
+    const int64_t need = partial_bytes(plan_for(WGRAD, s.ni, s.nj, s.nc), s.ni, s.nj);
     if (!workspace_ok(need, workspace, workspace_bytes)) return ZERO_EINVAL;
     const Span sy = my.span(), sx = mx.span(), sd = mw.span(), sb = mb.span(),
                sw = need ? span_of(workspace, need, 1) : Span{0, 0};
@@ -801,7 +902,6 @@ zero_status zero_linear_wgrad(const void *dy, zero_dtype dt, int64_t lddy, const
     a.e.out_f32 = gdt == ZERO_FP32;
     a.e.db = db;
     a.e.accumulate = accumulate != 0;
-    a.e.vec = quads(mw);
     return launch<WGRAD>(a, dt, stream);
 }
 

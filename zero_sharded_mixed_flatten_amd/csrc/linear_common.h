@@ -42,51 +42,56 @@ struct FP16 {
     }
 };
 
-// four elements as fp32, and back; n < 4 touches the first n only
+// Four elements as fp32, and back; n < 4 touches the first n only.  Whole
+// quads are one access whatever their alignment, which global memory takes.
 template <class T>
-__device__ __forceinline__ f32x4 load16(const uint16_t *p, int n, bool vec) {
+__device__ __forceinline__ f32x4 load16(const uint16_t *p, int n) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (vec && n == 4) {
-        const u16x4 h = *reinterpret_cast<const u16x4 *>(p);
+    if (n == 4) {
+        u16x4 h;
+        __builtin_memcpy(&h, p, 8);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = T::up(h[e]);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 3; ++e)
             if (e < n) v[e] = T::up(p[e]);
     }
     return v;
 }
 
 template <class T>
-__device__ __forceinline__ void store16(uint16_t *p, f32x4 v, int n, bool vec) {
+__device__ __forceinline__ void store16(uint16_t *p, f32x4 v, int n) {
     u16x4 h;
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[e] = T::down(v[e]);
-    if (vec && n == 4) {
-        *reinterpret_cast<u16x4 *>(p) = h;
+    if (n == 4) {
+        __builtin_memcpy(p, &h, 8);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 3; ++e)
             if (e < n) p[e] = h[e];
     }
 }
 
-__device__ __forceinline__ f32x4 load32(const float *p, int n, bool vec) {
-    if (vec && n == 4) return *reinterpret_cast<const f32x4 *>(p);
+__device__ __forceinline__ f32x4 load32(const float *p, int n) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (n == 4) {
+        __builtin_memcpy(&v, p, 16);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < n) v[e] = p[e];
+        for (int e = 0; e < 3; ++e)
+            if (e < n) v[e] = p[e];
+    }
     return v;
 }
 
-__device__ __forceinline__ void store32(float *p, f32x4 v, int n, bool vec) {
-    if (vec && n == 4) {
-        *reinterpret_cast<f32x4 *>(p) = v;
+__device__ __forceinline__ void store32(float *p, f32x4 v, int n) {
+    if (n == 4) {
+        __builtin_memcpy(p, &v, 16);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 3; ++e)
             if (e < n) p[e] = v[e];
     }
 }
