@@ -136,6 +136,86 @@ __device__ __forceinline__ void emit_pair(const Epilogue &e, int64_t i, int64_t 
     if (j1 < nj) emit<OP, T>(e, i, j1, static_cast<int>(nj - j1 < 4 ? nj - j1 : 4), v1, words, 1);
 }
 
+// eight neighbouring outputs (i, j..j+7), n of them inside: the quads at j
+// and j + 4, whose mask words are w0 and w1, the same half of both
+template <int OP, class T>
+__device__ __forceinline__ void emit8(const Epilogue &e, int64_t i, int64_t j, int n, f32x4 v0,
+                                      f32x4 v1, u32x4 w0, u32x4 w1, int half) {
+    if (n < 8) {
+        emit<OP, T>(e, i, j, n < 4 ? n : 4, v0, w0, half);
+        if (n > 4) emit<OP, T>(e, i, j + 4, n - 4, v1, w1, half);
+        return;
+    }
+    f32x4 a, b;
+    if constexpr (OP == WGRAD) {
+        if (e.out_f32) {
+            emit<OP, T>(e, i, j, 4, v0, w0, half);
+            emit<OP, T>(e, i, j + 4, 4, v1, w1, half);
+        } else {
+            uint16_t *o = static_cast<uint16_t *>(e.out) + i * e.ldo + j;
+            if (e.accumulate) {
+                load16x8<T>(o, a, b);
+                v0 = a + v0;
+                v1 = b + v1;
+            }
+            store16x8<T>(o, v0, v1);
+        }
+        return;
+    }
+    if constexpr (OP == FWD) {
+        if (e.bias != nullptr) {
+            load16x8<T>(e.bias + j, a, b);
+            v0 += a;
+            v1 += b;
+        }
+        if (e.z != nullptr) store16x8<T>(e.z + i * e.ldz + j, v0, v1);
+        if (e.act != ZERO_ACT_NONE) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v0[k] = act_value(v0[k], e.act);
+                v1[k] = act_value(v1[k], e.act);
+            }
+        }
+    } else if (e.act != ZERO_ACT_NONE) {
+        load16x8<T>(e.z + i * e.ldz + j, a, b);
+        if (e.act == ZERO_ACT_RELU) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v0[k] = a[k] > 0.0f ? v0[k] : 0.0f;
+                v1[k] = b[k] > 0.0f ? v1[k] : 0.0f;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v0[k] *= act_slope(a[k], e.act);
+                v1[k] *= act_slope(b[k], e.act);
+            }
+        }
+    }
+    if (e.drop.on) {
+        v0 = drop_apply(e.drop, w0, half, v0);
+        v1 = drop_apply(e.drop, w1, half, v1);
+    }
+    if (e.out_f32) {
+        float *o = static_cast<float *>(e.out) + i * e.ldo + j;
+        if (e.res != nullptr) {
+            const float *r = static_cast<const float *>(e.res) + i * e.ldr + j;
+            v0 = load32(r, 4) + v0;
+            v1 = load32(r + 4, 4) + v1;
+        }
+        store32(o, v0, 4);
+        store32(o + 4, v1, 4);
+    } else {
+        uint16_t *o = static_cast<uint16_t *>(e.out) + i * e.ldo + j;
+        if (e.res != nullptr) {
+            load16x8<T>(static_cast<const uint16_t *>(e.res) + i * e.ldr + j, a, b);
+            v0 = a + v0;
+            v1 = b + v1;
+        }
+        store16x8<T>(o, v0, v1);
+    }
+}
+
 template <class T>
 __device__ __forceinline__ void emit_db(const Epilogue &e, int64_t i, float v) {
     if (e.out_f32) {
@@ -150,19 +230,30 @@ __device__ __forceinline__ void emit_db(const Epilogue &e, int64_t i, float v) {
 // ---------------------------------------------------------------------------
 // tiles in shared memory, in 16-byte pieces of eight elements
 //
-// Rows of c: [ROWS][64], piece (row, s) at row * 8 + (s ^ (row & 7)); a
-// lane's operand is one piece, eight consecutive c of its row.  The exclusive
-// or spreads the pieces that eight lanes read at once over all banks.
+// Which 16 rows of Q make a block is free, and is chosen for the outputs: row
+// 4 g + r of blocks t = 2 p and 2 p + 1 is j = 32 p + 8 g + 4 (t & 1) + r, so
+// that the two blocks leave a lane eight consecutive j of its i, and its four
+// neighbours the 64 bytes that follow (Q = true below).  Blocks of P are 16
+// consecutive rows.
+//
+// Rows of c: [ROWS][64], piece (row, s) at row * 8 + (s ^ twist(row)); a
+// lane's operand is one piece, eight consecutive c of its row.  twist differs
+// for any eight rows that are read at once, which spreads their pieces over
+// all banks.
 //
 // Rows of lanes: [64][ROWS], in 32-byte units of 16 lanes.
-// ds_read_b64_tr_b16 reads four rows of a unit and hands every lane the four
-// c of its own column; two of them make an operand.  The four rows must lie
-// in different banks: unit u of row c is stored at u ^ flip(c), and tiles of
-// 256 lanes, whose rows are two bank widths long, also skip 32 bytes after
-// each 1024 (a wave's direct copy is 1024 bytes, so it is not cut).  flip
-// touches few bits and depends on c mod 4 only, so that a lane's addresses
-// are one or two registers plus constants.
+// ds_read_b64_tr_b16 reads 4 x 4 quads, one of four rows c each, and hands
+// every lane the four c of its own column; two of them make an operand.  The
+// four rows must lie in different banks: unit u of row c is stored at
+// u ^ flip(c), and tiles of 256 lanes, whose rows are two bank widths long,
+// also skip 64 bytes after each 1024 (a wave's direct copy is 1024 bytes, so
+// it is not cut).  flip touches few bits and depends on c mod 4 only, so that
+// a lane's addresses are one or two registers plus constants.
 
+template <bool Q>
+__device__ __forceinline__ int twist(int row) {
+    return Q ? (row & 3) | (row >> 1 & 4) : row & 7;
+}
 template <int ROWS>
 constexpr int kFlipBits = ROWS == 256 ? 4 : ROWS == 128 ? 6 : 1;
 template <int ROWS>
@@ -170,7 +261,7 @@ __device__ __forceinline__ int flip(int c) {
     return ROWS == 256 ? (c & 1) * 4 : ROWS == 128 ? (c & 3) * 2 : (c >> 1) & 1;
 }
 template <bool KC, int ROWS>
-constexpr int kSkip = !KC && ROWS == 256 ? 16 : 0;  // elements after each 512
+constexpr int kSkip = !KC && ROWS == 256 ? 32 : 0;  // elements after each 512
 template <bool KC, int ROWS>
 constexpr int kTile = ROWS * kBK + ROWS * kBK / 512 * kSkip<KC, ROWS>;
 
@@ -178,9 +269,9 @@ template <bool KC, int ROWS>
 __device__ __forceinline__ int piece_row(int pos) {
     return KC ? pos >> 3 : pos / (ROWS / 8);
 }
-template <bool KC, int ROWS>
+template <bool KC, int ROWS, bool Q>
 __device__ __forceinline__ int piece_slot(int pos) {
-    if (KC) return (pos & 7) ^ ((pos >> 3) & 7);
+    if (KC) return (pos & 7) ^ twist<Q>(pos >> 3);
     return (pos % (ROWS / 8)) ^ (2 * flip<ROWS>(pos / (ROWS / 8)));
 }
 
@@ -206,7 +297,7 @@ __device__ __forceinline__ u32x4 load_piece(const uint16_t *p, int64_t n) {
     return v;
 }
 
-template <bool KC, int ROWS, int THREADS>
+template <bool KC, int ROWS, int THREADS, bool Q>
 struct Stage {
     static constexpr int N = ROWS * kBK / 8 / THREADS;
     static_assert(N >= 1 && N * THREADS * 8 == ROWS * kBK, "whole pieces for every thread");
@@ -217,7 +308,7 @@ struct Stage {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int pos = n * THREADS + static_cast<int>(threadIdx.x);
-            const int row = piece_row<KC, ROWS>(pos), s = piece_slot<KC, ROWS>(pos);
+            const int row = piece_row<KC, ROWS>(pos), s = piece_slot<KC, ROWS, Q>(pos);
             if (KC) {
                 const int64_t r = r0 + row, c = c0 + s * 8;
                 v[n] = load_piece(p + r * ld + c, r < rows ? c1 - c : 0);
@@ -242,7 +333,7 @@ struct Stage {
 // written out because the compiler makes every later read of shared memory
 // wait for all copies it knows of; the kernel waits for the ones it needs.
 // It has no output register, and its inputs are read when it issues.
-template <bool KC, int ROWS, int THREADS>
+template <bool KC, int ROWS, int THREADS, bool Q>
 struct Direct {
     static constexpr int N = ROWS * kBK / 8 / THREADS;
     static constexpr int kRows = THREADS * 8 / ROWS;  // rows of lanes per copy
@@ -260,7 +351,7 @@ struct Direct {
 #pragma unroll
         for (int n = 0; n < (KC ? N : 1); ++n) {
             const int pos = n * THREADS + static_cast<int>(threadIdx.x);
-            const int row = piece_row<KC, ROWS>(pos), s = piece_slot<KC, ROWS>(pos);
+            const int row = piece_row<KC, ROWS>(pos), s = piece_slot<KC, ROWS, Q>(pos);
             off[n] = KC ? static_cast<uint32_t>(min(row, last)) * static_cast<uint32_t>(ld * 2) + s * 16
                         : static_cast<uint32_t>(row) * static_cast<uint32_t>(ld * 2) +
                               min(s * 8, last) * 2;
@@ -279,24 +370,29 @@ struct Direct {
 
 // a lane's operand of 16-row block f from row row0 on: its eight consecutive
 // c of the 32 that start at kk * 32
-template <bool KC, int ROWS>
+template <bool KC, int ROWS, bool Q>
 __device__ __forceinline__ s16x8 fragment(const uint16_t *tile, int row0, int f, int kk, int lane) {
+    const int t = lane & 15, g = lane >> 4;
     if constexpr (KC) {
-        const int r = lane & 15, s = kk * 4 + (lane >> 4);
-        return *reinterpret_cast<const s16x8 *>(tile + (row0 + r) * kBK + ((s ^ (r & 7)) * 8) +
-                                                f * 16 * kBK);
+        const int r = Q ? (t >> 2) * 8 + (t & 3) : t;
+        const int first = Q ? (f >> 1) * 32 + (f & 1) * 4 : f * 16;
+        return *reinterpret_cast<const s16x8 *>(
+            tile + (row0 + r) * kBK + (((kk * 4 + g) ^ twist<Q>(r)) * 8) + first * kBK);
     } else {
-        const int t = lane & 15, c = (lane >> 4) * 8 + (t >> 2);
+        const int c = g * 8 + (t >> 2);
         constexpr int F = kFlipBits<ROWS>;
+        const int unit = Q ? (f >> 1) * 2 : f;      // of the block's first lane
+        const int in = Q ? (t & 3) >> 1 : 0;        // units on
         const int at = c * ROWS + (c * ROWS >> 9) * kSkip<KC, ROWS> +
-                       ((row0 / 16 + (f & F)) ^ flip<ROWS>(c)) * 16 + (t & 3) * 4;
+                       ((row0 / 16 + (unit & F) + in) ^ flip<ROWS>(c)) * 16 +
+                       (Q ? (t & 1) * 8 + (f & 1) * 4 : (t & 3) * 4);
         using lds4 = __attribute__((address_space(3))) s16x4;
         s16x8 v;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             constexpr int per_row = ROWS + ROWS * kSkip<KC, ROWS> / 512;
             const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds4 *)(tile + at + (f & ~F) * 16 + (kk * 32 + h * 4) * per_row));
+                (lds4 *)(tile + at + (unit & ~F) * 16 + (kk * 32 + h * 4) * per_row));
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[h * 4 + e] = x[e];
         }
@@ -369,11 +465,11 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     // whole steps go straight to shared memory (DIRECT); a last broken one is
     // staged through registers
     const int whole = DIRECT ? static_cast<int>((c1 - c0) / kBK) : 0;
-    Stage<PKC, BI, THREADS> sp;
-    Stage<QKC, BJ, THREADS> sq;
-    Direct<PKC, BI, THREADS> dp;
-    Direct<QKC, BJ, THREADS> dq;
-    constexpr int NP = Direct<PKC, BI, THREADS>::N, NQ = Direct<QKC, BJ, THREADS>::N;
+    Stage<PKC, BI, THREADS, false> sp;
+    Stage<QKC, BJ, THREADS, true> sq;
+    Direct<PKC, BI, THREADS, false> dp;
+    Direct<QKC, BJ, THREADS, true> dq;
+    constexpr int NP = Direct<PKC, BI, THREADS, false>::N, NQ = Direct<QKC, BJ, THREADS, true>::N;
     if (DIRECT) {
         dp.init(a.p, a.ldp, i0, a.ni, c0);
         dq.init(a.q, a.ldq, j0, a.nj, c0);
@@ -403,9 +499,9 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     auto read = [&](int n, int s, int kk) __attribute__((always_inline)) {
         const uint16_t *tp = tiles + slot_of(s), *tq = tp + kTile<PKC, BI>;
         if (n < FJ)
-            fq[kk][n] = fragment<QKC, BJ>(tq, wj, n, kk, lane);
+            fq[kk][n] = fragment<QKC, BJ, true>(tq, wj, n, kk, lane);
         else if (n < FJ + FI)
-            fp[kk][n - FJ] = fragment<PKC, BI>(tp, wi, n - FJ, kk, lane);
+            fp[kk][n - FJ] = fragment<PKC, BI, false>(tp, wi, n - FJ, kk, lane);
     };
     // the products of half kk, with reads of half 1 - kk of step rs and (COPY)
     // copies of step cs between them
@@ -525,12 +621,29 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
                 for (int t = 0; t < FJ; ++t) v[t] = acc[s][t];
             }
         const int64_t i = i0 + wi + f * 16 + (lane & 15);
+        // A lane has quads 2 g and 2 g + 1 of each 32 columns; quad u takes
+        // the mask block u % 4.  The four lanes of a row draw one block each
+        // and hand them round, while all of them are there.
+        u32x4 w0[FJ / 2], w1[FJ / 2];
+        if (OP != WGRAD && a.e.drop.on && a.parts == 1) {
+#pragma unroll
+            for (int p = 0; p < FJ / 2; ++p) {
+                const u32x4 w = drop_words(a.e.drop, stream, static_cast<uint32_t>(i),
+                                           static_cast<uint32_t>((j0 + wj) / 8 + p * 4 + g));
+                const int from = (lane & 15) + 16 * ((2 * g) & 3);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    w0[p][k] = static_cast<uint32_t>(__shfl(static_cast<int>(w[k]), from));
+                    w1[p][k] = static_cast<uint32_t>(__shfl(static_cast<int>(w[k]), from + 16));
+                }
+            }
+        }
         if (i >= a.ni) continue;
         if (a.parts > 1) {
             float *row = a.partial + (part * a.ni + i) * njp;
 #pragma unroll
             for (int t = 0; t < FJ; ++t) {
-                const int64_t j = j0 + wj + t * 16 + g * 4;
+                const int64_t j = j0 + wj + (t >> 1) * 32 + g * 8 + (t & 1) * 4;
                 if (j < a.nj) *reinterpret_cast<f32x4 *>(row + j) = v[t];
             }
             if (DB && with_db && g == f >> 2)
@@ -538,8 +651,12 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
             continue;
         }
 #pragma unroll
-        for (int t = 0; t < FJ; t += 2)
-            emit_pair<OP, T>(a.e, i, j0 + wj + t * 16 + g * 4, a.nj, stream, v[t], v[t + 1]);
+        for (int p = 0; p < FJ / 2; ++p) {
+            const int64_t j = j0 + wj + p * 32 + g * 8;
+            if (j < a.nj)
+                emit8<OP, T>(a.e, i, j, static_cast<int>(min(a.nj - j, int64_t(8))), v[2 * p],
+                             v[2 * p + 1], w0[p], w1[p], g >> 1);
+        }
         if (DB && with_db && g == f >> 2) emit_db<T>(a.e, i, sum_of(f));
     }
 }

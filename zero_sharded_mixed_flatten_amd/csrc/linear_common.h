@@ -96,6 +96,31 @@ __device__ __forceinline__ void store32(float *p, f32x4 v, int n) {
     }
 }
 
+// eight elements at once
+using u16x8 = uint16_t __attribute__((ext_vector_type(8)));
+
+template <class T>
+__device__ __forceinline__ void load16x8(const uint16_t *p, f32x4 &a, f32x4 &b) {
+    u16x8 h;
+    __builtin_memcpy(&h, p, 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        a[e] = T::up(h[e]);
+        b[e] = T::up(h[e + 4]);
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store16x8(uint16_t *p, f32x4 a, f32x4 b) {
+    u16x8 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = T::down(a[e]);
+        h[e + 4] = T::down(b[e]);
+    }
+    __builtin_memcpy(p, &h, 16);
+}
+
 // ---------------------------------------------------------------------------
 // dropout
 
