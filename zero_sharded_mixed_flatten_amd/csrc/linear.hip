@@ -783,8 +783,26 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
     if (op == FWD && ni <= 32) return Plan{ni <= 16 ? 16 : 32, 16, 1, nc};
+    // 256 x 256 tiles read least from shared memory a product, but only one
+    // fits a CU: nothing runs under its epilogue and the last round may be
+    // thin.  128 x 128 tiles run two to a CU and fill the card evenly.
+    // Modelled times (us; steps of 64 and the epilogue as so many more) and
+    // measured ones, large : small tiles:
+    //   8192 x 4096 x 11008  590 : 655, measured 540 : 735
+    //   4096 x 4096 x 4096   117 : 128, measured 114 : 121
+    //   8192 x 6400 x 1600   187 : 168, measured 193 : 177
+    //   8192 x 1600 x 6400   165 : 160, measured 188 : 165
     Plan p{256, 256, 1, 0};
-    if (ceil_div(ni, 256) * ceil_div(nj, 256) < kCUs * 3 / 4) p.bi = p.bj = 128;
+    const double k = static_cast<double>(ceil_div(nc, kBK));
+    const int64_t large = ceil_div(ni, 256) * ceil_div(nj, 256);
+    const int64_t small = ceil_div(ni, 128) * ceil_div(nj, 128);
+    const int64_t rest = large % kCUs;
+    const double rounds =
+        large <= kCUs ? 1.0
+                      : static_cast<double>(large / kCUs) +
+                            (rest == 0 ? 0.0 : rest <= kCUs / 2 ? 0.55 : 0.5 + 0.5 * rest / kCUs);
+    if (std::max(1.0, small / (2.0 * kCUs) + 0.05) * (k + 4) * 0.92 < rounds * (k + 7) * 1.65)
+        p.bi = p.bj = 128;
     if (ni <= 64) p.bi = 64;
     const int64_t tiles = ceil_div(ni, p.bi) * ceil_div(nj, p.bj);
     const int64_t steps = ceil_div(nc, kBK);

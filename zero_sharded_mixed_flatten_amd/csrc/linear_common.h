@@ -179,43 +179,53 @@ __device__ __forceinline__ f32x4 drop_apply(const Drop &d, u32x4 w, int half, f3
 // 2^-22, below the half step 2^-11 of the finest 16-bit output; with an fp32
 // output it is the largest error of the call.
 
-__device__ __forceinline__ float sigmoid(float u) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504088896341f));
+// The epilogues are bound by these instructions (a 256 x 256 tile's outputs
+// wait for them alone), so the constants are folded and multiply-adds fused.
+
+// 1 / (1 + 2^w)
+__device__ __forceinline__ float logistic(float w) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(w));
 }
+constexpr float kLog2e = 1.44269504088896341f;
+// GELU_TANH: (1 + tanh(u / 2)) / 2 = logistic(-u log2 e) with
+// u = v (kTanh1 + kTanh3 v^2), and du/dv = kTanh1 + 3 kTanh3 v^2
+constexpr float kTanh1 = 1.5957691216057308f, kTanh3 = kTanh1 * 0.044715f;
 
 __device__ __forceinline__ float act_value(float v, int act) {
     switch (act) {
         case ZERO_ACT_RELU: return v > 0.0f ? v : (v != v ? v : 0.0f);
         case ZERO_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-        case ZERO_ACT_GELU_TANH:  // (1 + tanh(u / 2)) / 2 = sigmoid(u)
-            return v * sigmoid(1.5957691216057308f * (v + 0.044715f * (v * v * v)));
-        case ZERO_ACT_SILU: return v * sigmoid(v);
+        case ZERO_ACT_GELU_TANH:
+            return v * logistic(v * __builtin_fmaf(-kLog2e * kTanh3, v * v, -kLog2e * kTanh1));
+        case ZERO_ACT_SILU: return v * logistic(-kLog2e * v);
         default: return v;
     }
 }
 
-// Where the bell factor of a derivative has vanished its product with v is 0
-// (0 * Inf would not be).
+// Where the bell factor t of a derivative has vanished its product with v is
+// 0 (0 * Inf would not be).
 __device__ __forceinline__ float act_slope(float v, int act) {
     float s, t, d;
     switch (act) {
         case ZERO_ACT_GELU:
-            s = 0.5f * (1.0f + erff(v * 0.70710678118654752f));
-            t = __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f);
+            s = __builtin_fmaf(0.5f, erff(v * 0.70710678118654752f), 0.5f);
+            t = __builtin_amdgcn_exp2f(v * v * (-0.5f * kLog2e));
             d = v * 0.39894228040143268f;
             break;
-        case ZERO_ACT_GELU_TANH:
-            s = sigmoid(1.5957691216057308f * (v + 0.044715f * (v * v * v)));
-            t = s * (1.0f - s);
-            d = v * (1.5957691216057308f * (1.0f + 0.134145f * (v * v)));
+        case ZERO_ACT_GELU_TANH: {
+            const float q = v * v;
+            s = logistic(v * __builtin_fmaf(-kLog2e * kTanh3, q, -kLog2e * kTanh1));
+            t = __builtin_fmaf(-s, s, s);
+            d = v * __builtin_fmaf(3.0f * kTanh3, q, kTanh1);
             break;
+        }
         default:  // SILU
-            s = sigmoid(v);
-            t = s * (1.0f - s);
+            s = logistic(-kLog2e * v);
+            t = __builtin_fmaf(-s, s, s);
             d = v;
             break;
     }
-    return t == 0.0f ? s : s + t * d;
+    return t == 0.0f ? s : __builtin_fmaf(t, d, s);
 }
 
 // ---------------------------------------------------------------------------
