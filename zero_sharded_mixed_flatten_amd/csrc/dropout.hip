@@ -1,10 +1,12 @@
 // dropout.hip -- gfx950 kernel of zero_dropout: y = residual + D(x) with the
 // counter-based mask of zero_linear.h, stored nowhere.
 //
-// One pass: a lane takes the two quads of a row that share a draw of the
-// mask (columns 4b.. and 16 + 4b.. of a group of 32), so eight elements cost
-// one Philox call, about 120 integer cycles of a SIMD against 32 bytes of
-// traffic (bf16); the pass is bound by HBM.
+// One pass, eight elements and one Philox call a lane.  fp32: the two quads
+// that share a draw (columns 4b.. and 16 + 4b.. of a group of 32), two
+// 16-byte accesses each 64 bytes contiguous over four lanes.  16-bit types:
+// eight neighbouring columns, one 16-byte access; the four lanes of a group
+// draw one block each and pass the words on by DPP.  (With the fp32 layout,
+// 8-byte accesses, 16384 x 4096 bf16 with a residual took 81 us, 4.97 TB/s.)
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -24,58 +26,101 @@ struct Args {
     Drop drop;
 };
 
-struct FP32 {};
+// This thread's row and lane of the row.  A workgroup is 256 consecutive
+// (row, lane) pairs; the one division is of its first pair, in scalar
+// registers, and rows shorter than a workgroup take a 32-bit one more.
+__device__ __forceinline__ bool place(const Args &a, int64_t &i, uint32_t &u) {
+    const int64_t lanes = (a.cols + 31) / 32 * 4, first = static_cast<int64_t>(blockIdx.x) * 256;
+    const int64_t i0 = first / lanes;
+    const uint32_t n = static_cast<uint32_t>(lanes);
+    const uint32_t at = static_cast<uint32_t>(first - i0 * lanes) + threadIdx.x;
+    const uint32_t rows = n >= 256 ? (at >= n ? 1u : 0u) : at / n;
+    i = i0 + rows;
+    u = at - rows * n;
+    return i < a.rows;
+}
+
+template <int CTRL>
+__device__ __forceinline__ u32x4 from_lane(u32x4 w) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        w[e] = static_cast<uint32_t>(
+            __builtin_amdgcn_update_dpp(0, static_cast<int>(w[e]), CTRL, 0xF, 0xF, false));
+    return w;
+}
 
 template <class T>
-struct Access {
-    static __device__ __forceinline__ f32x4 load(const void *p, int64_t at, int n) {
-        return load16<T>(static_cast<const uint16_t *>(p) + at, n);
+__global__ void __launch_bounds__(256) dropout16_kernel(Args a) {
+    int64_t i;
+    uint32_t u;
+    if (!place(a, i, u)) return;  // whole groups of four lanes
+    const int64_t j = static_cast<int64_t>(u) * 8;
+    const uint16_t *x = static_cast<const uint16_t *>(a.x) + i * a.ldx + j;
+    const uint16_t *r = static_cast<const uint16_t *>(a.res) + i * a.ldr + j;
+    const bool whole = j + 8 <= a.cols, res = a.res != nullptr;
+    const int n0 = static_cast<int>(j >= a.cols ? 0 : a.cols - j < 4 ? a.cols - j : 4);
+    const int n1 = static_cast<int>(j + 4 >= a.cols ? 0 : a.cols - j - 4);
+    f32x4 v0, v1, r0 = {0.f, 0.f, 0.f, 0.f}, r1 = r0;
+    if (whole) {
+        load16x8<T>(x, v0, v1);
+        if (res) load16x8<T>(r, r0, r1);
+    } else {
+        v0 = load16<T>(x, n0);
+        v1 = load16<T>(x + 4, n1);
+        if (res) {
+            r0 = load16<T>(r, n0);
+            r1 = load16<T>(r + 4, n1);
+        }
     }
-    static __device__ __forceinline__ void store(void *p, int64_t at, f32x4 v, int n) {
-        store16<T>(static_cast<uint16_t *>(p) + at, v, n);
+    if (a.drop.on) {
+        const u32x4 w = drop_words(a.drop, drop_stream(a.drop), static_cast<uint32_t>(i), u);
+        // quads 2 q and 2 q + 1 of the group: blocks 0, 2, 0, 2 and 1, 3, 1, 3
+        const int half = static_cast<int>(u >> 1) & 1;
+        v0 = drop_apply(a.drop, from_lane<0x88>(w), half, v0);
+        v1 = drop_apply(a.drop, from_lane<0xDD>(w), half, v1);
     }
-};
-template <>
-struct Access<FP32> {
-    static __device__ __forceinline__ f32x4 load(const void *p, int64_t at, int n) {
-        return load32(static_cast<const float *>(p) + at, n);
+    if (res) {
+        v0 = r0 + v0;
+        v1 = r1 + v1;
     }
-    static __device__ __forceinline__ void store(void *p, int64_t at, f32x4 v, int n) {
-        store32(static_cast<float *>(p) + at, v, n);
+    uint16_t *y = static_cast<uint16_t *>(a.y) + i * a.ldy + j;
+    if (whole) {
+        store16x8<T>(y, v0, v1);
+    } else {
+        store16<T>(y, v0, n0);
+        store16<T>(y + 4, v1, n1);
     }
-};
+}
 
-template <class T>
-__global__ void __launch_bounds__(256) dropout_kernel(Args a) {
-    using A = Access<T>;
-    const int64_t quads = (a.cols + 31) / 32 * 4;
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (id >= a.rows * quads) return;
-    const int64_t i = id / quads, u = id - i * quads;
-    const int64_t j = u / 4 * 32 + u % 4 * 4;
+__global__ void __launch_bounds__(256) dropout32_kernel(Args a) {
+    const float *x = static_cast<const float *>(a.x), *res = static_cast<const float *>(a.res);
+    float *y = static_cast<float *>(a.y);
+    int64_t i;
+    uint32_t u;
+    if (!place(a, i, u)) return;
+    const int64_t j = static_cast<int64_t>(u / 4) * 32 + u % 4 * 4;
     if (j >= a.cols) return;
     const int n0 = static_cast<int>(a.cols - j < 4 ? a.cols - j : 4);
     const int64_t left = a.cols - j - 16;
     const int n1 = static_cast<int>(left < 0 ? 0 : left < 4 ? left : 4);
-    f32x4 v0 = A::load(a.x, i * a.ldx + j, n0);
-    f32x4 v1 = A::load(a.x, i * a.ldx + j + 16, n1);
+    f32x4 v0 = load32(x + i * a.ldx + j, n0);
+    f32x4 v1 = load32(x + i * a.ldx + j + 16, n1);
     f32x4 r0 = {0.f, 0.f, 0.f, 0.f}, r1 = r0;
-    if (a.res != nullptr) {
-        r0 = A::load(a.res, i * a.ldr + j, n0);
-        r1 = A::load(a.res, i * a.ldr + j + 16, n1);
+    if (res != nullptr) {
+        r0 = load32(res + i * a.ldr + j, n0);
+        r1 = load32(res + i * a.ldr + j + 16, n1);
     }
     if (a.drop.on) {
-        const u32x4 w = drop_words(a.drop, drop_stream(a.drop), static_cast<uint32_t>(i),
-                                   static_cast<uint32_t>(u));
+        const u32x4 w = drop_words(a.drop, drop_stream(a.drop), static_cast<uint32_t>(i), u);
         v0 = drop_apply(a.drop, w, 0, v0);
         v1 = drop_apply(a.drop, w, 1, v1);
     }
-    if (a.res != nullptr) {
+    if (res != nullptr) {
         v0 = r0 + v0;
         v1 = r1 + v1;
     }
-    A::store(a.y, i * a.ldy + j, v0, n0);
-    A::store(a.y, i * a.ldy + j + 16, v1, n1);
+    store32(y + i * a.ldy + j, v0, n0);
+    store32(y + i * a.ldy + j + 16, v1, n1);
 }
 
 }  // namespace
@@ -112,10 +157,10 @@ extern "C" zero_status zero_dropout(const void *x, zero_dtype dt, int64_t ldx, i
     const int64_t blocks = (rows * quads + 255) / 256;
     if (blocks > 0x7FFFFFFF) return ZERO_EINVAL;
     if (dt == ZERO_BF16)
-        dropout_kernel<BF16><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(a);
+        dropout16_kernel<BF16><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(a);
     else if (dt == ZERO_FP16)
-        dropout_kernel<FP16><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(a);
+        dropout16_kernel<FP16><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(a);
     else
-        dropout_kernel<FP32><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(a);
+        dropout32_kernel<<<static_cast<uint32_t>(blocks), 256, 0, st>>>(a);
     return launch_status();
 }

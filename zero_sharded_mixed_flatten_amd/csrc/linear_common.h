@@ -131,6 +131,12 @@ struct Drop {
     const int64_t *step;
 };
 
+// a ^ b ^ c in one instruction (0x96: the truth table of the three)
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+    return static_cast<uint32_t>(__builtin_amdgcn_bitop3_b32(
+        static_cast<int>(a), static_cast<int>(b), static_cast<int>(c), 0x96));
+}
+
 // Philox4x32-10 (the generator of Salmon et al., 2011): ten rounds of two
 // 32 x 32 -> 64 bit products.  Integer work of about 20 full products for
 // eight mask elements.
@@ -140,9 +146,9 @@ __device__ __forceinline__ u32x4 philox(uint32_t c0, uint32_t c1, uint32_t c2, u
     for (int r = 0; r < 10; ++r) {
         const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0;
         const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
-        c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
+        c0 = xor3(static_cast<uint32_t>(p1 >> 32), c1, k0);
         c1 = static_cast<uint32_t>(p1);
-        c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
+        c2 = xor3(static_cast<uint32_t>(p0 >> 32), c3, k1);
         c3 = static_cast<uint32_t>(p0);
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
