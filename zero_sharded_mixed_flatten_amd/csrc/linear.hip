@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
         for (int n = 0; n < FI + FJ; ++n) read(n, 0, 0);
 #pragma unroll 1
         for (int s = 0; s < steps; ++s) {
-            if (s + 1 < steps) put(s + 1);
             half(first{}, std::false_type{}, s, 0);
+            if (s + 1 < steps) put(s + 1);
             arrive();
             if (s + 2 < steps) load(s + 2);
             half(second{}, std::false_type{}, s + 1, 0);
@@ -783,33 +783,35 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
     if (op == FWD && ni <= 32) return Plan{ni <= 16 ? 16 : 32, 16, 1, nc};
-    // 256 x 256 tiles read least from shared memory a product, but only one
-    // fits a CU: nothing runs under its epilogue and the last round may be
-    // thin.  128 x 128 tiles run two to a CU and fill the card evenly.
-    // Modelled times (us; steps of 64 and the epilogue as so many more) and
-    // measured ones, large : small tiles:
-    //   8192 x 4096 x 11008  590 : 655, measured 540 : 735
-    //   4096 x 4096 x 4096   117 : 128, measured 114 : 121
-    //   8192 x 6400 x 1600   187 : 168, measured 193 : 177
-    //   8192 x 1600 x 6400   165 : 160, measured 188 : 165
-    Plan p{256, 256, 1, 0};
-    const double k = static_cast<double>(ceil_div(nc, kBK));
+    const int64_t steps = std::max<int64_t>(ceil_div(nc, kBK), 1);
+    // 256 x 256 tiles read least from shared memory and from memory a
+    // product, but one fills a CU.  They pay from five eighths of a round on
+    // (2500 x 4096 x 4096, 160 of them: 98 us, 128 x 128 tiles 100;
+    // 8192 x 6400 x 1600: 200 : 215) and where the main loop outweighs the
+    // epilogue (wgrad 11008 x 4096 over 64 and 256 rows: 66 : 53 and 80 : 62;
+    // 6400 x 1600, 175 tiles, over 512 rows 32 : 25 and over 8192 193 : 222;
+    // 4096 x 4096, a whole round, over 512 rows 33 : 35).
     const int64_t large = ceil_div(ni, 256) * ceil_div(nj, 256);
-    const int64_t small = ceil_div(ni, 128) * ceil_div(nj, 128);
-    const int64_t rest = large % kCUs;
-    const double rounds =
-        large <= kCUs ? 1.0
-                      : static_cast<double>(large / kCUs) +
-                            (rest == 0 ? 0.0 : rest <= kCUs / 2 ? 0.55 : 0.5 + 0.5 * rest / kCUs);
-    if (std::max(1.0, small / (2.0 * kCUs) + 0.05) * (k + 4) * 0.92 < rounds * (k + 7) * 1.65)
-        p.bi = p.bj = 128;
-    if (ni <= 64) p.bi = 64;
+    if (large >= kCUs * 5 / 8 && steps > (large >= kCUs ? 4 : 8))
+        return Plan{256, 256, 1, steps * kBK};
+    Plan p{ni <= 64 ? 64 : 128, 128, 1, 0};
+    // Parts of the contraction, while all of them fit the card at once.  A
+    // step takes 0.62 us with one workgroup on a CU and 0.95 with two, and
+    // joining costs 4 us and 0.5 a part: 128 x 4096 x 4096 in 1 (no parts), 8
+    // and 16: 45, 19.7 and 24.8 us; wgrad 1600 x 1600 over 4096 rows in 1 and
+    // 3: 47 and 36; 512 x 6400 x 1600 in 1 and 2: 23.5 and 26.5.
     const int64_t tiles = ceil_div(ni, p.bi) * ceil_div(nj, p.bj);
-    const int64_t steps = ceil_div(nc, kBK);
     int64_t parts = 1;
-    if (tiles < kCUs) parts = std::min<int64_t>(2 * kCUs / std::max<int64_t>(tiles, 1), steps / 4);
-    parts = std::max<int64_t>(1, std::min<int64_t>(parts, 64));
-    p.chunk = std::max<int64_t>(ceil_div(steps, parts), 1) * kBK;
+    double best = 0.0;
+    for (int64_t n = 1; n <= 64 && n <= steps && (n == 1 || tiles * n <= 2 * kCUs); ++n) {
+        const double cost = static_cast<double>(ceil_div(steps, n)) * (tiles * n <= kCUs ? 0.62 : 0.95) +
+                            (n == 1 ? 0.0 : 4.0 + 0.5 * static_cast<double>(n));
+        if (n == 1 || cost < best) {
+            best = cost;
+            parts = n;
+        }
+    }
+    p.chunk = ceil_div(steps, parts) * kBK;
     p.parts = static_cast<int>(std::max<int64_t>(1, ceil_div(nc, p.chunk)));
     return p;
 }
