@@ -326,3 +326,82 @@ def test_gradients_agree_with_differences():
             # z and dz were rounded to fp16: 2^-11 of dz each, and dz moves by
             # at most |z| 2^-11 |silu''| |c| (|silu''| <= 0.5)
             assert abs(mine - diff) <= 6 * 2.0 ** -11 * size, (which, trial, mine, diff)
+
+
+def test_offsets_past_32_bits():
+    """rows 2^30 + 8 elements apart (the last starts past 2^32 bytes), read
+    and written in place"""
+    ld, m, n, k = (1 << 30) + 8, 4, 40, 72
+    x, w = whole(m, k, 1), whole(n, k, 2)
+    buf = torch.zeros((m - 1) * ld + 256, dtype=torch.bfloat16, device="cuda")
+    bx = buf.as_strided((m, k), (ld, 1), 0)
+    by = buf.as_strided((m, n), (ld, 1), 128)   # between the rows of x
+    bx.copy_(x)
+    bw = w.to(torch.bfloat16).cuda()
+    want = product64(x, w).to(torch.bfloat16)
+    with pytest.raises(zs.ZeroValueError):      # their spans overlap
+        zs.zero_linear(bx, bw, by)
+    y = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    zs.zero_linear(bx, bw, y)
+    assert torch.equal(y.cpu(), want)
+    big = torch.zeros((40 - 1) * (1 << 26) + 256, dtype=torch.bfloat16, device="cuda")
+    xs = whole(40, k, 3)                         # the tile kernel's rows, 128 MiB apart
+    far = big.as_strided((40, k), (1 << 26, 1), 0)
+    far.copy_(xs)
+    y2 = torch.empty(40, n, dtype=torch.float32, device="cuda")
+    zs.zero_linear(far, bw, y2)
+    assert torch.equal(y2.cpu().double(), product64(xs, w))
+    dw = torch.empty(n, k, dtype=torch.float32, device="cuda")
+    dy = whole(40, n, 4)
+    zs.zero_linear_wgrad(dy.to(torch.bfloat16).cuda(), far, dw)
+    assert torch.equal(dw.cpu().double(), product64(dy.t().contiguous(), xs.t().contiguous()))
+    out = big.as_strided((40, n), (1 << 26, 1), 128)
+    zs.zero_linear(xs.to(torch.bfloat16).cuda(), bw, out)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu().double(), product64(xs, w).to(torch.bfloat16).double())
+    zs.zero_dropout(out, out, zs.ZeroDropout(0.5, 3))
+    keep = ref.keep(40, n, 0.5, 3, 0)
+    assert torch.equal(out.cpu() != 0, keep & (product64(xs, w).to(torch.bfloat16) != 0))
+
+
+def test_calls_in_turn_share_a_workspace():
+    """products with divided contractions one after another on one scratch"""
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    shapes = [(40, 96, 5000), (64, 200, 3000), (33, 40, 8191), (40, 96, 5000)]
+    outs = []
+    for i, (m, n, k) in enumerate(shapes):
+        assert 0 < zs.zero_linear_workspace_bytes(zs.ZERO_LINEAR, m, n, k) <= ws.numel()
+        x, w = whole(m, k, i), whole(n, k, i + 9)
+        y = torch.empty(m, n, device="cuda")
+        zs.zero_linear(x.to(torch.bfloat16).cuda(), w.to(torch.bfloat16).cuda(), y, workspace=ws)
+        outs.append((y, product64(x, w)))
+    torch.cuda.synchronize()
+    for y, want in outs:
+        assert torch.equal(y.cpu().double(), want)
+
+
+def test_the_binding_refuses_before_a_launch():
+    x, w = (torch.ones(s, dtype=torch.bfloat16, device="cuda") for s in ((40, 64), (48, 64)))
+    y = torch.full((40, 48), CANARY, dtype=torch.bfloat16, device="cuda")
+    bad = [(TypeError, dict(y=y.to(torch.float16))), (ValueError, dict(y=y[:39])),
+           (ValueError, dict(w=w[:, :60])), (TypeError, dict(w=w.half())),
+           (TypeError, dict(w=torch.ones(64, 48, dtype=torch.bfloat16, device="cuda").t())),
+           (TypeError, dict(x=x[0])), (TypeError, dict(x=x[:1].expand(40, 64))),
+           (ValueError, dict(bias=w[0, :40])), (TypeError, dict(bias=w[0].float())),
+           (ValueError, dict(residual=y[:, :40])), (TypeError, dict(residual=y.float())),
+           (ValueError, dict(z=y[:3])), (ValueError, dict(act=9)),
+           (ValueError, dict(drop=zs.ZeroDropout(1.0))),
+           (TypeError, dict(drop=zs.ZeroDropout(0.1, step=torch.ones(1, device="cuda")))),
+           (ValueError, dict(y=x.view(-1)[:40 * 48].view(40, 48)))]
+    for err, change in bad:
+        args = {**dict(x=x, w=w, y=y), **change}
+        with pytest.raises(err):
+            zs.zero_linear(args.pop("x"), args.pop("w"), args.pop("y"), **args)
+    long = torch.ones(40, 8192, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        zs.zero_linear(long, long[:8], y[:, :8],
+                       workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        zs.zero_linear_dgrad(y, w, x, act=zs.ZERO_ACT_SILU)
+    torch.cuda.synchronize()
+    assert bool((y == CANARY).all())
