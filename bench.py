@@ -68,14 +68,16 @@ def parse():
     p.add_argument("--flags", action="store_true",
                    help="single-launch steps: also raise the overflow flag and sum the squares "
                         "of the scaled gradient (the shard's part of the global norm)")
-    p.add_argument("--op", choices=["step", "reshard", "consolidate", "quantize", "dequantize"],
+    p.add_argument("--op", choices=["step", "reshard", "consolidate", "quantize", "dequantize",
+                                    "block"],
                    default="step",
                    help="step: the optimizer step (default); reshard: new rank 5 of 16's "
                         "shard of the 7B fp32 master, m and v from the 8-rank shards; "
                         "consolidate: the 8-rank fp32 master shards scattered into the "
                         "7B model's 291 per-parameter fp32 tensors; quantize / dequantize: "
                         "the 8-bit codec on rank 1's fp32 gradient of the 7B shard (to int8 "
-                        "blocks, and back to bf16)")
+                        "blocks, and back to bf16); block: forward and backward of one "
+                        "MLP block of the GPT-2-XL list on the flat buffers, 8192 tokens")
     p.add_argument("--calibrate-copy", type=int, default=0, metavar="MIB",
                    help="only run a plain device-to-device copy of MIB MiB (the known-size "
                         "reference that scales the HBM byte counters) --steps times and exit")
@@ -505,6 +507,8 @@ def main():
     if args.calibrate_copy:
         calibrate_copy(args.calibrate_copy, args.steps)
         return
+    if args.op == "block":
+        return bench_block(args)
     if args.op in ("quantize", "dequantize"):
         bench_codec(args)
         return
@@ -788,6 +792,78 @@ def bench_codec(args):
                                 "sample": f"the first {n} elements of the shard, {reps} calls, "
                                           f"single-threaded C oracle ({dt:.1f} s)"}
     print(json.dumps(line), flush=True)
+
+
+def bench_block(args):
+    """What a rank runs between two sharded steps, for one block: the first
+    MLP of the GPT-2-XL list (1600 -> 6400 -> 1600, biases, GELU, dropout 0.1
+    into the residual) on 8192 tokens, forward and backward.  The weights are
+    read from the flat bf16 buffer of the whole list and the gradients written
+    to their places in a flat bf16 row: five products of 2 m d ffn flops (the
+    block's input gradient is the neighbour's business), the dropout's
+    backward and the step counter."""
+    import torch
+
+    import zero_sharded_mixed_flatten_amd as zs
+    from synth.workloads import gpt2xl_numels
+
+    m, d, f = 8192, 1600, 6400
+    numels = gpt2xl_numels()
+    lay, offs = zs.zero_flatten_layout(numels, 1)
+    up = next(i for i in range(len(numels) - 3)
+              if [numels[i + k] for k in range(4)] == [d * f, f, f * d, d])
+    g = torch.Generator(device="cuda").manual_seed(0)
+    weights = torch.zeros(lay.n_pad, dtype=torch.bfloat16, device="cuda")
+    row = torch.zeros(lay.n_pad, dtype=torch.bfloat16, device="cuda")
+
+    def part(buf, i, *shape):
+        return buf[int(offs[i]):int(offs[i]) + numels[i]].view(*shape)
+
+    def rand(*shape, sigma=1.0):
+        return (torch.randn(*shape, generator=g, device="cuda") * sigma).to(torch.bfloat16)
+
+    w1, b1, w2, b2 = (part(weights, up, f, d), part(weights, up + 1, f),
+                      part(weights, up + 2, d, f), part(weights, up + 3, d))
+    g1, gb1, g2, gb2 = (part(row, up, f, d), part(row, up + 1, f), part(row, up + 2, d, f),
+                        part(row, up + 3, d))
+    for w in (w1, b1, w2, b2):
+        w.copy_(rand(*w.shape, sigma=0.02))
+    x, c = rand(m, d), rand(m, d, sigma=1e-3)
+    h, z, dz = (torch.empty(m, f, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    y, dy = torch.empty_like(x), torch.empty_like(x)
+    t = zs.new_step_counter(1)
+    drop = zs.ZeroDropout(0.1, seed=1, step=t)
+    act = zs.ZERO_ACT_GELU_TANH
+    ws = torch.empty(max(1, *(zs.zero_linear_workspace_bytes(op, m, n, k)
+                              for op in (zs.ZERO_LINEAR, zs.ZERO_LINEAR_DGRAD,
+                                         zs.ZERO_LINEAR_WGRAD)
+                              for n, k in ((f, d), (d, f)))), dtype=torch.uint8, device="cuda")
+
+    def step():
+        zs.zero_linear(x, w1, h, bias=b1, act=act, z=z, workspace=ws)
+        zs.zero_linear(h, w2, y, bias=b2, drop=drop, residual=x, workspace=ws)
+        zs.zero_dropout(c, dy, drop)
+        zs.zero_linear_wgrad(dy, h, g2, db=gb2, workspace=ws)
+        zs.zero_linear_dgrad(dy, w2, dz, act=act, z=z, workspace=ws)
+        zs.zero_linear_wgrad(dz, x, g1, db=gb1, workspace=ws)
+        zs.zero_step_counter_advance(t)
+
+    for _ in range(args.warmup):
+        step()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    for _ in range(args.steps):
+        step()
+    torch.cuda.synchronize()
+    ms = (time.perf_counter() - t0) / args.steps * 1e3
+    flops = 5 * 2 * m * d * f
+    print(json.dumps({
+        "metric": "MLP block forward and backward on the flat buffers, tokens/s",
+        "value": m / ms * 1e3, "unit": "tokens/s", "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True, "scaling": "weak",
+        "vs_baseline": None, "dtype": "bf16", "data": "synthetic", "tflops": flops / ms / 1e9,
+        "config": {"model": "gpt2xl_mlp_block", "tokens": m, "d": d, "ffn": f, "dropout": 0.1,
+                   "parallelism": "one rank"}}), flush=True)
 
 
 def cpu_baseline_copy(op, s8, n):

@@ -455,12 +455,18 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     for (int f = 0; f < FI; ++f)
 #pragma unroll
         for (int t = 0; t < FJ; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // The column sums of dy are one more product: block f's operand with a
-    // matrix whose row f is ones, so that one accumulator's 16 rows hold the
-    // sums of all FI blocks.
-    f32x4 sums = {0.f, 0.f, 0.f, 0.f};
-    static_assert(FI <= 16, "a row of the sums for every block");
-    const bool with_db = DB && tj == 0 && wj == 0;
+    // The column sums of dy are one more product of P's blocks, with a matrix
+    // of ones.  The waves of a row of the tile share these blocks: each sums
+    // SUMS of them, which it reads once more (its turn picks them, and
+    // registers cannot be picked without branches).
+    constexpr int SUMS = FI / WJ;
+    static_assert(!DB || (FI % WJ == 0 && SUMS <= 2), "the waves share the blocks of P");
+    f32x4 sums[DB ? SUMS : 1];
+    s16x8 fs[2][DB ? SUMS : 1];
+#pragma unroll
+    for (int e = 0; e < (DB ? SUMS : 1); ++e) sums[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const bool with_db = DB && tj == 0;
+    const int turn = wave % WJ;
 
     // whole steps go straight to shared memory (DIRECT); a last broken one is
     // staged through registers
@@ -505,7 +511,7 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     };
     // the products of half kk, with reads of half 1 - kk of step rs and (COPY)
     // copies of step cs between them
-    auto half = [&](auto kk_, auto copy_, int rs, int cs) __attribute__((always_inline)) {
+    auto half = [&](auto kk_, auto copy_, auto db_, int rs, int cs) __attribute__((always_inline)) {
         constexpr int kk = decltype(kk_)::value, READS = FI + FJ, N = FI * FJ;
         constexpr bool COPY = decltype(copy_)::value;
 #pragma unroll
@@ -527,15 +533,21 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
                         placed = true;
                     }
             }
-            acc[n / FJ][n % FJ] = mfma<T>(fq[kk][n % FJ], fp[kk][n / FJ], acc[n / FJ][n % FJ]);
-            if (placed) __builtin_amdgcn_sched_barrier(0);
-        }
-        if (DB && with_db) {
+            if (decltype(db_)::value && kk == 0 && n == 0) {
 #pragma unroll
-            for (int f = 0; f < FI; ++f) {
-                const short o = (lane & 15) == f ? static_cast<short>(T::down(1.0f)) : short(0);
-                sums = mfma<T>(s16x8{o, o, o, o, o, o, o, o}, fp[kk][f], sums);
+                for (int e = 0; e < 2 * SUMS; ++e)
+                    fs[e & 1][e / 2] = fragment<PKC, BI, false>(
+                        tiles + slot_of(rs), wi + (turn * SUMS + e / 2) * 16, 0, e & 1, lane);
             }
+            acc[n / FJ][n % FJ] = mfma<T>(fq[kk][n % FJ], fp[kk][n / FJ], acc[n / FJ][n % FJ]);
+            if (decltype(db_)::value && kk == 0 && n == N - 1) {
+                const short o = static_cast<short>(T::down(1.0f));
+#pragma unroll
+                for (int e = 0; e < 2 * SUMS; ++e)
+                    sums[e / 2] = mfma<T>(s16x8{o, o, o, o, o, o, o, o}, fs[e & 1][e / 2],
+                                          sums[e / 2]);
+            }
+            if (placed) __builtin_amdgcn_sched_barrier(0);
         }
     };
     using first = std::integral_constant<int, 0>;
@@ -549,65 +561,72 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    if constexpr (DIRECT) {
-        if (whole > 0) {
+    auto contract = [&](auto db) __attribute__((always_inline)) {
+        if constexpr (DIRECT) {
+            if (whole > 0) {
 #pragma unroll
-            for (int n = 0; n < NP + NQ; ++n) copy(n, 0);
-            copied();
-            arrive();
-            if (whole > 1) {
-#pragma unroll
-                for (int n = 0; n < NP + NQ; ++n) copy(n, 1);
+                for (int n = 0; n < NP + NQ; ++n) copy(n, 0);
                 copied();
+                arrive();
+                if (whole > 1) {
+#pragma unroll
+                    for (int n = 0; n < NP + NQ; ++n) copy(n, 1);
+                    copied();
+                }
+#pragma unroll
+                for (int n = 0; n < FI + FJ; ++n) read(n, 0, 0);
+                int s = 0;
+#pragma unroll 1
+                for (; s < whole - 2; ++s) {
+                    half(first{}, std::false_type{}, db, s, 0);
+                    arrive();
+                    half(second{}, std::true_type{}, db, s + 1, s + 2);
+                    copied();
+                }
+#pragma unroll 1
+                for (; s < whole; ++s) {
+                    half(first{}, std::false_type{}, db, s, 0);
+                    arrive();
+                    half(second{}, std::false_type{}, db, s + 1, 0);
+                }
             }
+            if (whole < steps) {  // the broken step, in the buffer nobody reads
+                load(whole);
+                put(whole);
+                arrive();
+#pragma unroll
+                for (int n = 0; n < FI + FJ; ++n) read(n, whole, 0);
+                half(first{}, std::false_type{}, db, whole, 0);
+                half(second{}, std::false_type{}, db, whole, 0);
+            }
+        } else if (steps > 0) {
+            load(0);
+            put(0);
+            arrive();
+            if (steps > 1) load(1);
 #pragma unroll
             for (int n = 0; n < FI + FJ; ++n) read(n, 0, 0);
-            int s = 0;
 #pragma unroll 1
-            for (; s < whole - 2; ++s) {
-                half(first{}, std::false_type{}, s, 0);
+            for (int s = 0; s < steps; ++s) {
+                half(first{}, std::false_type{}, db, s, 0);
+                if (s + 1 < steps) put(s + 1);
                 arrive();
-                half(second{}, std::true_type{}, s + 1, s + 2);
-                copied();
-            }
-#pragma unroll 1
-            for (; s < whole; ++s) {
-                half(first{}, std::false_type{}, s, 0);
-                arrive();
-                half(second{}, std::false_type{}, s + 1, 0);
+                if (s + 2 < steps) load(s + 2);
+                half(second{}, std::false_type{}, db, s + 1, 0);
             }
         }
-        if (whole < steps) {  // the broken step, in the buffer nobody reads
-            load(whole);
-            put(whole);
-            arrive();
-#pragma unroll
-            for (int n = 0; n < FI + FJ; ++n) read(n, whole, 0);
-            half(first{}, std::false_type{}, whole, 0);
-            half(second{}, std::false_type{}, whole, 0);
-        }
-    } else if (steps > 0) {
-        load(0);
-        put(0);
-        arrive();
-        if (steps > 1) load(1);
-#pragma unroll
-        for (int n = 0; n < FI + FJ; ++n) read(n, 0, 0);
-#pragma unroll 1
-        for (int s = 0; s < steps; ++s) {
-            half(first{}, std::false_type{}, s, 0);
-            if (s + 1 < steps) put(s + 1);
-            arrive();
-            if (s + 2 < steps) load(s + 2);
-            half(second{}, std::false_type{}, s + 1, 0);
-        }
-    }
+    };
+    // two loops, so that the other tiles' has no branch of the sums' in it
+    if (with_db)
+        contract(std::integral_constant<bool, DB>{});
+    else
+        contract(std::false_type{});
 
     const int g = lane >> 4;
     const int64_t njp = padded4(a.nj);
     const uint64_t stream = OP != WGRAD && a.e.drop.on && a.parts == 1 ? drop_stream(a.e.drop) : 0;
     auto sum_of = [&](int f) __attribute__((always_inline)) {
-        return (f & 2) ? ((f & 1) ? sums[3] : sums[2]) : ((f & 1) ? sums[1] : sums[0]);
+        return DB && SUMS == 2 && (f & 1) ? sums[DB ? SUMS - 1 : 0][0] : sums[0][0];
     };
     // one body for all rows of blocks: the block's registers are selected by
     // uniform branches
@@ -646,7 +665,7 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
                 const int64_t j = j0 + wj + (t >> 1) * 32 + g * 8 + (t & 1) * 4;
                 if (j < a.nj) *reinterpret_cast<f32x4 *>(row + j) = v[t];
             }
-            if (DB && with_db && g == f >> 2)
+            if (DB && with_db && f / SUMS == turn && g == 0)
                 a.partial[a.parts * a.ni * njp + part * a.ni + i] = sum_of(f);
             continue;
         }
@@ -657,7 +676,7 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
                 emit8<OP, T>(a.e, i, j, static_cast<int>(min(a.nj - j, int64_t(8))), v[2 * p],
                              v[2 * p + 1], w0[p], w1[p], g >> 1);
         }
-        if (DB && with_db && g == f >> 2) emit_db<T>(a.e, i, sum_of(f));
+        if (DB && with_db && f / SUMS == turn && g == 0) emit_db<T>(a.e, i, sum_of(f));
     }
 }
 
