@@ -19,8 +19,10 @@
  *  - A matrix argument is its first element and a row stride ld in elements;
  *    elements of a row are contiguous.  Nothing between a row's end and the
  *    next row's start is read or written.
- *  - Dimensions are 0 <= m, n, k <= 2^31 - 1024, and a matrix spans at most
- *    2^60 elements.  An empty output is a no-op; an empty contraction gives
+ *  - A matrix occupies its span, from its first element to one past its last:
+ *    two matrices that interleave (column ranges of one buffer) overlap.
+ *  - Dimensions are 0 <= m, n, k <= 2^31 - 1024, a matrix spans at most 2^60
+ *    elements, and a product has less than 2^23 output tiles of 64 x 128.  An empty output is a no-op; an empty contraction gives
  *    sums of zero.
  *  - Products of 16-bit elements are exact in fp32 and are summed in fp32 by
  *    the matrix instructions; bias, activation, dropout and residual are
@@ -128,7 +130,7 @@ ZERO_API zero_status zero_linear_dgrad(const void *dy, zero_dtype dt, int64_t ld
  * micro-batch); db[n] likewise from the column sums of dy, or NULL.
  *   dw, db: type gdt: dt, or FP32 (an fp32 gradient row).  Accumulation adds
  *           the fp32 sum to the widened old value and rounds once.
- * Errors as for zero_linear. */
+ * Errors as for zero_linear; EINVAL also for a db where k is 0. */
 ZERO_API zero_status zero_linear_wgrad(const void *dy, zero_dtype dt, int64_t lddy, const void *x,
                                        int64_t ldx, int64_t m, int64_t n, int64_t k, void *dw,
                                        zero_dtype gdt, int64_t lddw, void *db, int32_t accumulate,

@@ -138,3 +138,17 @@ def test_a_captured_graph_draws_a_new_mask_every_replay():
         torch.cuda.synchronize()
         assert torch.equal(y, eager) and torch.equal(h, eh)
         assert torch.equal(y.cpu(), _want(x.cpu(), None, 0.4, 31, 1000 + step))
+
+
+def test_more_than_one_launch():
+    """2^33 elements and more go out as several launches; the last rows and
+    those about the first launch's end against the definition"""
+    rows, cols = (1 << 21) + 37, 4096
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+    zs.zero_dropout(x, x, zs.ZeroDropout(0.5, 8))
+    torch.cuda.synchronize()
+    for first in (0, (1 << 21) - 8, rows - 16):
+        keep = ref.keep(16, cols, 0.5, 8, 0, first)
+        assert torch.equal(x[first:first + 16].cpu() != 0, keep)
+    del x
+    torch.cuda.empty_cache()

@@ -119,6 +119,8 @@ LONG = dict(m=40, n=8, k=1 << 16)   # a divided contraction for linear
     ("linear", dict(LONG, ldx=1 << 16, ldw=1 << 16, ws=at(5)), EALIAS),
     ("linear", dict(LONG, ldx=1 << 16, ldw=1 << 16, ws=at(4)), EALIAS),
     ("linear", dict(LONG, ldx=1 << 16, ldw=1 << 16, ws=at(6)), EALIAS),
+    # more output tiles than one launch takes
+    ("dgrad", dict(m=1, n=1, k=BIG, ldw=BIG, lddx=BIG, act=0, res=None), EINVAL),
     ("dgrad", dict(dt=2), EINVAL), ("dgrad", dict(dxdt=1), EINVAL), ("dgrad", dict(z=None), EINVAL),
     ("dgrad", dict(lddy=47), EINVAL), ("dgrad", dict(lddx=63), EINVAL),
     ("dgrad", dict(ldz=63), EINVAL), ("dgrad", dict(act=7), EINVAL),

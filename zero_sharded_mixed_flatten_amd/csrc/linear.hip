@@ -625,8 +625,10 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     const int g = lane >> 4;
     const int64_t njp = padded4(a.nj);
     const uint64_t stream = OP != WGRAD && a.e.drop.on && a.parts == 1 ? drop_stream(a.e.drop) : 0;
+    // values, not places: an array picked from by address would go to memory
+    const float sum0 = sums[0][0], sum1 = sums[DB ? SUMS - 1 : 0][0];
     auto sum_of = [&](int f) __attribute__((always_inline)) {
-        return DB && SUMS == 2 && (f & 1) ? sums[DB ? SUMS - 1 : 0][0] : sums[0][0];
+        return SUMS == 2 && (f & 1) ? sum1 : sum0;
     };
     // one body for all rows of blocks: the block's registers are selected by
     // uniform branches
@@ -792,6 +794,7 @@ __global__ void __launch_bounds__(256) join_kernel(Args a) {
 // host
 
 constexpr int kCUs = 256;
+constexpr int64_t kMaxTiles = int64_t(1) << 23;  // a launch has less than 2^32 threads
 
 struct Plan {
     int bi, bj, parts;  // bi == 16 or 32: the kernel for few rows
@@ -801,7 +804,8 @@ struct Plan {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
-    if (op == FWD && ni <= 32) return Plan{ni <= 16 ? 16 : 32, 16, 1, nc};
+    if (op == FWD && ni <= 32 && nj < (int64_t(1) << 26))
+        return Plan{ni <= 16 ? 16 : 32, 16, 1, nc};
     const int64_t steps = std::max<int64_t>(ceil_div(nc, kBK), 1);
     // 256 x 256 tiles read least from shared memory and from memory a
     // product, but one fills a CU.  They pay from five eighths of a round on
@@ -862,7 +866,7 @@ zero_status run_tiles(Args &a, hipStream_t st) {
     a.tiles_j = static_cast<int32_t>(ceil_div(a.nj, BJ));
     a.quarter = -1;
     const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j;
-    if (tiles > 0x7FFFFFFF) return ZERO_EINVAL;
+    if (tiles >= kMaxTiles) return ZERO_EINVAL;
     // One of the largest tiles occupies a CU.  What is left after the last
     // whole round of them, up to half a round, runs as quarters, two to a CU.
     const int64_t rest = tiles % kCUs;
