@@ -158,7 +158,7 @@ __device__ __forceinline__ void emit8(const Epilogue &e, int64_t i, int64_t j, i
                 v0 = a + v0;
                 v1 = b + v1;
             }
-            store16x8<T>(o, v0, v1);
+            stream16x8<T>(o, v0, v1);
         }
         return;
     }
@@ -168,7 +168,7 @@ __device__ __forceinline__ void emit8(const Epilogue &e, int64_t i, int64_t j, i
             v0 += a;
             v1 += b;
         }
-        if (e.z != nullptr) store16x8<T>(e.z + i * e.ldz + j, v0, v1);
+        if (e.z != nullptr) stream16x8<T>(e.z + i * e.ldz + j, v0, v1);
         if (e.act != ZERO_ACT_NONE) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -212,7 +212,48 @@ __device__ __forceinline__ void emit8(const Epilogue &e, int64_t i, int64_t j, i
             v0 = a + v0;
             v1 = b + v1;
         }
-        store16x8<T>(o, v0, v1);
+        stream16x8<T>(o, v0, v1);
+    }
+}
+
+// eight whole outputs without a mask, and without activation or with one of
+// the two logistic ones (ACT)
+template <int OP, class T, bool ACT>
+__device__ __forceinline__ void emit_light(const Epilogue &e, int64_t i, int64_t j, f32x4 v0,
+                                           f32x4 v1, const Logistic &l) {
+    f32x4 a, b;
+    if (OP == FWD && e.bias != nullptr) {
+        load16x8<T>(e.bias + j, a, b);
+        v0 += a;
+        v1 += b;
+    }
+    if (OP == FWD && e.z != nullptr) stream16x8<T>(e.z + i * e.ldz + j, v0, v1);
+    if (ACT && OP == DGRAD) load16x8<T>(e.z + i * e.ldz + j, a, b);
+    if (ACT) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v0[k] = OP == FWD ? logistic_value(v0[k], l) : v0[k] * logistic_slope(a[k], l);
+            v1[k] = OP == FWD ? logistic_value(v1[k], l) : v1[k] * logistic_slope(b[k], l);
+        }
+    }
+    const bool add = OP == WGRAD ? e.accumulate != 0 : e.res != nullptr;
+    const void *old = OP == WGRAD ? e.out : e.res;
+    const int64_t at = i * (OP == WGRAD ? e.ldo : e.ldr) + j;
+    if (e.out_f32) {
+        if (add) {
+            v0 = load32(static_cast<const float *>(old) + at, 4) + v0;
+            v1 = load32(static_cast<const float *>(old) + at + 4, 4) + v1;
+        }
+        float *o = static_cast<float *>(e.out) + i * e.ldo + j;
+        store32(o, v0, 4);
+        store32(o + 4, v1, 4);
+    } else {
+        if (add) {
+            load16x8<T>(static_cast<const uint16_t *>(old) + at, a, b);
+            v0 = a + v0;
+            v1 = b + v1;
+        }
+        stream16x8<T>(static_cast<uint16_t *>(e.out) + i * e.ldo + j, v0, v1);
     }
 }
 
@@ -630,6 +671,34 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     auto sum_of = [&](int f) __attribute__((always_inline)) {
         return SUMS == 2 && (f & 1) ? sum1 : sum0;
     };
+    // Outputs without a mask are written by straight code, without a register
+    // to move (8192 x 6400 x 1600: 205 -> 158 us); columns that are not eight
+    // whole ones are left to the body below.  Only as much as the instruction
+    // cache holds: with every activation and the masks it loses (242 -> 252).
+    const bool smooth = a.e.act == ZERO_ACT_GELU_TANH || a.e.act == ZERO_ACT_SILU;
+    const bool light = a.parts == 1 && !a.e.drop.on && (a.e.act == ZERO_ACT_NONE || smooth);
+    if (light) {
+        const Logistic l = logistic_of(a.e.act);
+        auto write = [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+            for (int f = 0; f < FI; ++f) {
+                const int64_t i = i0 + wi + f * 16 + (lane & 15);
+#pragma unroll
+                for (int p = 0; p < FJ / 2; ++p) {
+                    const int64_t j = j0 + wj + p * 32 + g * 8;
+                    if (i < a.ni && j + 8 <= a.nj)
+                        emit_light<OP, T, decltype(act)::value>(a.e, i, j, acc[f][2 * p],
+                                                                acc[f][2 * p + 1], l);
+                }
+            }
+        };
+        if (OP != WGRAD && smooth)
+            write(std::integral_constant<bool, OP != WGRAD>{});
+        else
+            write(std::false_type{});
+        const bool edge = (a.nj & 7) != 0 && j0 + BJ > a.nj;
+        if (!edge && !with_db) return;
+    }
     // one body for all rows of blocks: the block's registers are selected by
     // uniform branches
 #pragma unroll 1
@@ -674,7 +743,7 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
 #pragma unroll
         for (int p = 0; p < FJ / 2; ++p) {
             const int64_t j = j0 + wj + p * 32 + g * 8;
-            if (j < a.nj)
+            if (j < a.nj && !(light && j + 8 <= a.nj))
                 emit8<OP, T>(a.e, i, j, static_cast<int>(min(a.nj - j, int64_t(8))), v[2 * p],
                              v[2 * p + 1], w0[p], w1[p], g >> 1);
         }
@@ -814,8 +883,11 @@ Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
     // epilogue (wgrad 11008 x 4096 over 64 and 256 rows: 66 : 53 and 80 : 62;
     // 6400 x 1600, 175 tiles, over 512 rows 32 : 25 and over 8192 193 : 222;
     // 4096 x 4096, a whole round, over 512 rows 33 : 35).
+    // Where they would hang further over the edges, the small ones:
+    // 333 x 50257 x 1600 122 : 98 us, 256 x 50257 x 1600 67 : 80.
     const int64_t large = ceil_div(ni, 256) * ceil_div(nj, 256);
-    if (large >= kCUs * 5 / 8 && steps > (large >= kCUs ? 4 : 8))
+    const int64_t small = ceil_div(ni, 128) * ceil_div(nj, 128);
+    if (large >= kCUs * 5 / 8 && 4 * large * 7 <= small * 8 && steps > (large >= kCUs ? 4 : 8))
         return Plan{256, 256, 1, steps * kBK};
     Plan p{ni <= 64 ? 64 : 128, 128, 1, 0};
     // Parts of the contraction, while all of them fit the card at once.  A
