@@ -216,11 +216,12 @@ __device__ __forceinline__ void emit8(const Epilogue &e, int64_t i, int64_t j, i
     }
 }
 
-// eight whole outputs without a mask, and without activation or with one of
-// the two logistic ones (ACT)
-template <int OP, class T, bool ACT>
+// eight whole outputs without activation or with one of the two logistic ones
+// (ACT), and with a mask (MASK: the words and half of emit8) or without
+template <int OP, class T, bool ACT, bool MASK>
 __device__ __forceinline__ void emit_light(const Epilogue &e, int64_t i, int64_t j, f32x4 v0,
-                                           f32x4 v1, const Logistic &l) {
+                                           f32x4 v1, const Logistic &l, u32x4 w0, u32x4 w1,
+                                           int half) {
     f32x4 a, b;
     if (OP == FWD && e.bias != nullptr) {
         load16x8<T>(e.bias + j, a, b);
@@ -235,6 +236,10 @@ __device__ __forceinline__ void emit_light(const Epilogue &e, int64_t i, int64_t
             v0[k] = OP == FWD ? logistic_value(v0[k], l) : v0[k] * logistic_slope(a[k], l);
             v1[k] = OP == FWD ? logistic_value(v1[k], l) : v1[k] * logistic_slope(b[k], l);
         }
+    }
+    if (MASK) {
+        v0 = drop_apply(e.drop, w0, half, v0);
+        v1 = drop_apply(e.drop, w1, half, v1);
     }
     const bool add = OP == WGRAD ? e.accumulate != 0 : e.res != nullptr;
     const void *old = OP == WGRAD ? e.out : e.res;
@@ -671,31 +676,53 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     auto sum_of = [&](int f) __attribute__((always_inline)) {
         return SUMS == 2 && (f & 1) ? sum1 : sum0;
     };
-    // Outputs without a mask are written by straight code, without a register
-    // to move (8192 x 6400 x 1600: 205 -> 158 us); columns that are not eight
-    // whole ones are left to the body below.  Only as much as the instruction
-    // cache holds: with every activation and the masks it loses (242 -> 252).
+    // A lane has quads 2 g and 2 g + 1 of each 32 columns; quad u takes the
+    // mask block u % 4.  The four lanes of a row draw one block each and hand
+    // them round, while all of them are there.
+    auto draw = [&](int64_t i, int p, u32x4 &w0, u32x4 &w1) __attribute__((always_inline)) {
+        const u32x4 w = drop_words(a.e.drop, stream, static_cast<uint32_t>(i),
+                                   static_cast<uint32_t>((j0 + wj) / 8 + p * 4 + g));
+        const int from = (lane & 15) + 16 * ((2 * g) & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w0[k] = static_cast<uint32_t>(__shfl(static_cast<int>(w[k]), from));
+            w1[k] = static_cast<uint32_t>(__shfl(static_cast<int>(w[k]), from + 16));
+        }
+    };
+    // The usual outputs are written by straight code, without a register to
+    // move (8192 x 6400 x 1600: 205 -> 158 us); columns that are not eight
+    // whole ones are left to the body below.  One such code for each kind,
+    // and no more than the instruction cache holds: one for every activation
+    // and mask together loses (with GELU and z 242 -> 252).
     const bool smooth = a.e.act == ZERO_ACT_GELU_TANH || a.e.act == ZERO_ACT_SILU;
-    const bool light = a.parts == 1 && !a.e.drop.on && (a.e.act == ZERO_ACT_NONE || smooth);
+    const bool masked = OP != WGRAD && a.e.drop.on;
+    const bool light =
+        a.parts == 1 && (a.e.act == ZERO_ACT_NONE || (smooth && !masked));
     if (light) {
         const Logistic l = logistic_of(a.e.act);
-        auto write = [&](auto act) __attribute__((always_inline)) {
+        auto write = [&](auto act, auto mask) __attribute__((always_inline)) {
+            constexpr bool MASK = decltype(mask)::value;
 #pragma unroll
             for (int f = 0; f < FI; ++f) {
                 const int64_t i = i0 + wi + f * 16 + (lane & 15);
 #pragma unroll
                 for (int p = 0; p < FJ / 2; ++p) {
                     const int64_t j = j0 + wj + p * 32 + g * 8;
+                    u32x4 w0 = {0u, 0u, 0u, 0u}, w1 = w0;
+                    if (MASK) draw(i, p, w0, w1);
                     if (i < a.ni && j + 8 <= a.nj)
-                        emit_light<OP, T, decltype(act)::value>(a.e, i, j, acc[f][2 * p],
-                                                                acc[f][2 * p + 1], l);
+                        emit_light<OP, T, decltype(act)::value, MASK>(
+                            a.e, i, j, acc[f][2 * p], acc[f][2 * p + 1], l, w0, w1, g >> 1);
                 }
             }
         };
+        using yes = std::integral_constant<bool, OP != WGRAD>;
         if (OP != WGRAD && smooth)
-            write(std::integral_constant<bool, OP != WGRAD>{});
+            write(yes{}, std::false_type{});
+        else if (masked)
+            write(std::false_type{}, yes{});
         else
-            write(std::false_type{});
+            write(std::false_type{}, std::false_type{});
         const bool edge = (a.nj & 7) != 0 && j0 + BJ > a.nj;
         if (!edge && !with_db) return;
     }
@@ -711,22 +738,10 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
                 for (int t = 0; t < FJ; ++t) v[t] = acc[s][t];
             }
         const int64_t i = i0 + wi + f * 16 + (lane & 15);
-        // A lane has quads 2 g and 2 g + 1 of each 32 columns; quad u takes
-        // the mask block u % 4.  The four lanes of a row draw one block each
-        // and hand them round, while all of them are there.
         u32x4 w0[FJ / 2], w1[FJ / 2];
         if (OP != WGRAD && a.e.drop.on && a.parts == 1) {
 #pragma unroll
-            for (int p = 0; p < FJ / 2; ++p) {
-                const u32x4 w = drop_words(a.e.drop, stream, static_cast<uint32_t>(i),
-                                           static_cast<uint32_t>((j0 + wj) / 8 + p * 4 + g));
-                const int from = (lane & 15) + 16 * ((2 * g) & 3);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    w0[p][k] = static_cast<uint32_t>(__shfl(static_cast<int>(w[k]), from));
-                    w1[p][k] = static_cast<uint32_t>(__shfl(static_cast<int>(w[k]), from + 16));
-                }
-            }
+            for (int p = 0; p < FJ / 2; ++p) draw(i, p, w0[p], w1[p]);
         }
         if (i >= a.ni) continue;
         if (a.parts > 1) {
