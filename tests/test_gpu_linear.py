@@ -405,3 +405,30 @@ def test_the_binding_refuses_before_a_launch():
         zs.zero_linear_dgrad(y, w, x, act=zs.ZERO_ACT_SILU)
     torch.cuda.synchronize()
     assert bool((y == CANARY).all())
+
+
+# undivided contractions without a mask, or with a mask and no activation: the
+# straight epilogues, at sizes inside one tile, off the tiles and of the largest
+STRAIGHT = [(70, 130, 64), (300, 520, 64), (129, 261, 50), (4104, 2600, 576)]
+
+
+@pytest.mark.parametrize("act,p", [("gelu_tanh", 0.0), ("silu", 0.0), ("none", 0.25)])
+@pytest.mark.parametrize("m,n,k", STRAIGHT)
+def test_straight_forward_epilogues(m, n, k, act, p):
+    assert zs.zero_linear_workspace_bytes(zs.ZERO_LINEAR, m, n, k) == 0
+    big = m > 1000
+    for dtype, out, bias, res, keep_z in (
+            ((torch.bfloat16, torch.bfloat16, True, True, True),) if big else
+            ((torch.bfloat16, torch.bfloat16, True, True, True),
+             (torch.float16, torch.float16, False, False, False),
+             (torch.bfloat16, torch.float32, True, True, False))):
+        _forward(m, n, k, dtype, out, act, p, bias, res, keep_z=keep_z)
+
+
+@pytest.mark.parametrize("act,p", [("gelu_tanh", 0.0), ("silu", 0.0), ("none", 0.25)])
+@pytest.mark.parametrize("m,k,n", STRAIGHT)
+def test_straight_dgrad_epilogues(m, n, k, act, p):
+    assert zs.zero_linear_workspace_bytes(zs.ZERO_LINEAR_DGRAD, m, n, k) == 0
+    _dgrad(m, n, k, torch.bfloat16, torch.bfloat16, act, p, True)
+    if m < 1000:
+        _dgrad(m, n, k, torch.float16, torch.float32, act, p, False)
