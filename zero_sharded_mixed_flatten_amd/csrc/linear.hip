@@ -893,13 +893,17 @@ Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
     const int64_t steps = std::max<int64_t>(ceil_div(nc, kBK), 1);
     // 256 x 256 tiles read least from shared memory and from memory a
     // product, but one fills a CU.  They pay from five eighths of a round on
-    // (2500 x 4096 x 4096, 160 of them: 98 us, 128 x 128 tiles 100;
-    // 8192 x 6400 x 1600: 200 : 215) and where the main loop outweighs the
-    // epilogue (wgrad 11008 x 4096 over 64 and 256 rows: 66 : 53 and 80 : 62;
-    // 6400 x 1600, 175 tiles, over 512 rows 32 : 25 and over 8192 193 : 222;
-    // 4096 x 4096, a whole round, over 512 rows 33 : 35).
-    // Where they would hang further over the edges, the small ones:
-    // 333 x 50257 x 1600 122 : 98 us, 256 x 50257 x 1600 67 : 80.
+    // and where the main loop outweighs the epilogue.  Times (us) with them
+    // and with 128 x 128 tiles, on inputs that change from call to call:
+    //   2500 x 4096 x 4096 (160 tiles)                 87 :  99
+    //   8192 x 6400 x 1600                            153 : 164
+    //   wgrad 6400 x 1600 over 8192 rows (175 tiles)  182 : 217
+    //   the same over 512 rows                       23.5 : 23.1
+    //   wgrad 4096 x 4096 over 512 rows (256 tiles)    29 :  34
+    //   wgrad 11008 x 4096 over 64 rows                52 :  50
+    //   256 x 50257 x 1600                             62 :  83
+    // and where they would hang further over the edges, the small ones:
+    //   333 x 50257 x 1600                            104 : 101
     const int64_t large = ceil_div(ni, 256) * ceil_div(nj, 256);
     const int64_t small = ceil_div(ni, 128) * ceil_div(nj, 128);
     if (large >= kCUs * 5 / 8 && 4 * large * 7 <= small * 8 && steps > (large >= kCUs ? 4 : 8))
@@ -907,9 +911,10 @@ Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
     Plan p{ni <= 64 ? 64 : 128, 128, 1, 0};
     // Parts of the contraction, while all of them fit the card at once.  A
     // step takes 0.62 us with one workgroup on a CU and 0.95 with two, and
-    // joining costs 4 us and 0.5 a part: 128 x 4096 x 4096 in 1 (no parts), 8
-    // and 16: 45, 19.7 and 24.8 us; wgrad 1600 x 1600 over 4096 rows in 1 and
-    // 3: 47 and 36; 512 x 6400 x 1600 in 1 and 2: 23.5 and 26.5.
+    // joining costs 4 us and 0.5 a part.  Undivided : divided as this says:
+    // 128 x 4096 x 4096 41 : 20 us (8 parts; 25 in 16), 64 x 4096 x 11008
+    // 124 : 29, wgrad 1600 x 1600 over 4096 rows 47 : 36; 512 x 6400 x 1600
+    // is left whole, 21 us (27 in 2).
     const int64_t tiles = ceil_div(ni, p.bi) * ceil_div(nj, p.bj);
     int64_t parts = 1;
     double best = 0.0;
