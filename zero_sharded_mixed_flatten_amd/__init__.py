@@ -282,14 +282,17 @@ def _torch_stream(stream, device):
 
 
 def _workspace(sumsq, workspace, length: int, device, stream=None):
-    """(pointer, bytes) of the sum's workspace: the caller's (checked for
-    size) or a new one; (NULL, 0) without a sum.  A new one is allocated on
-    the call's stream: it is freed when the call returns, and torch's
-    allocator reuses a block only in the order of the stream it was
-    allocated on, so the call's kernels finish with it first."""
+    """(tensor, pointer, bytes) of the sum's workspace: the caller's (checked
+    for size) or a new one; (None, NULL, 0) without a sum.  A new one is
+    allocated on the call's stream and held by the entry point until its
+    kernels are enqueued (freed before, another thread could be handed its
+    block first: the library is called without the interpreter's lock): it is
+    freed when the call returns, and torch's allocator reuses a block only in
+    the order of the stream it was allocated on, so the call's kernels finish
+    with it first."""
     import torch
     if sumsq is None:
-        return None, 0
+        return None, None, 0
     need = zero_sumsq_workspace_bytes(max(0, length))
     if workspace is None:
         with torch.cuda.stream(_torch_stream(stream, device)):
@@ -297,7 +300,7 @@ def _workspace(sumsq, workspace, length: int, device, stream=None):
     nbytes = workspace.numel() * workspace.element_size()
     if nbytes < need:
         raise ValueError(f"workspace: {need} bytes needed, the tensor holds {nbytes}")
-    return _buf(workspace, "workspace", 0, device=device), nbytes
+    return workspace, _buf(workspace, "workspace", 0, device=device), nbytes
 
 
 def _stream(stream, like):
@@ -389,7 +392,7 @@ def zero_shard_reduce(grads, n_contrib: int, ld: int, length: int, acc,
     zero_sumsq_workspace_bytes(length) bytes is passed)."""
     import torch
     d = acc.device
-    ws, ws_bytes = _workspace(sumsq, workspace, length, d, stream)
+    held, ws, ws_bytes = _workspace(sumsq, workspace, length, d, stream)
     _check(_lib.zero_shard_reduce(
         _rows(grads, "grads", n_contrib, ld, length, device=d),
         _dtype_code(grads, "grads", True), n_contrib, ld, length,
@@ -471,7 +474,7 @@ def zero_shard_step(grads, ld: int, length: int, master, m, v, weight_full,
     import torch
     hpc = hp._c()
     d = master.device
-    ws, ws_bytes = _workspace(sumsq, workspace, length, d, stream)
+    held, ws, ws_bytes = _workspace(sumsq, workspace, length, d, stream)
     _check(_lib.zero_shard_step(
         _rows(grads, "grads", layout.n_dp, ld, length, device=d),
         _dtype_code(grads, "grads", True), ld, length,
@@ -579,7 +582,7 @@ def zero_shard_step_dc(grads, ld: int, length: int, master, m, v, weight_full,
     (see zero_step_consts_make) when the kernels run."""
     import torch
     d = master.device
-    ws, ws_bytes = _workspace(sumsq, workspace, length, d, stream)
+    held, ws, ws_bytes = _workspace(sumsq, workspace, length, d, stream)
     _check(_lib.zero_shard_step_dc(
         _rows(grads, "grads", layout.n_dp, ld, length, device=d),
         _dtype_code(grads, "grads", True), ld, length,
@@ -702,7 +705,7 @@ def zero_shard_step_q8(gq, gscales, ld: int, sld: int, length: int, master, m, v
     import torch
     hpc = hp._c()
     d = master.device
-    ws, ws_bytes = _workspace(sumsq, workspace, length, d, stream)
+    held, ws, ws_bytes = _workspace(sumsq, workspace, length, d, stream)
     nb = q8_blocks(length)
     end = _slot_end(layout, rank, shard_off, length)
     _check(_lib.zero_shard_step_q8(
@@ -725,7 +728,7 @@ def zero_shard_step_q8_dc(gq, gscales, ld: int, sld: int, length: int, master, m
     consts (see zero_step_consts_make) when the kernels run."""
     import torch
     d = master.device
-    ws, ws_bytes = _workspace(sumsq, workspace, length, d, stream)
+    held, ws, ws_bytes = _workspace(sumsq, workspace, length, d, stream)
     nb = q8_blocks(length)
     end = _slot_end(layout, rank, shard_off, length)
     _check(_lib.zero_shard_step_q8_dc(

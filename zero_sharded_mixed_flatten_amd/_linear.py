@@ -130,17 +130,19 @@ def zero_linear_workspace_bytes(op: int, m: int, n: int, k: int) -> int:
 
 
 def _scratch(op, m, n, k, workspace, stream, device):
-    """(address, bytes) of the product's workspace: the caller's, or a new
-    one allocated on the call's stream (so that freeing it on return is
-    ordered after the kernels)."""
+    """(tensor, address, bytes) of the product's workspace: the caller's, or a
+    new one allocated on the call's stream.  The caller holds the tensor until
+    its kernels are enqueued: freed after that, its block is reused in the
+    stream's order, behind them; freed before, another thread could be handed
+    it first (the library is called without the interpreter's lock)."""
     if workspace is None:
         need = _lib.zero_linear_workspace_bytes(op, m, n, k)
         if need <= 0:
-            return None, 0
+            return None, None, 0
         with torch.cuda.stream(_torch_stream(stream, device)):
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        return workspace.data_ptr(), need
-    return _buf(workspace, "workspace", 0, device=device).value, \
+        return workspace, workspace.data_ptr(), need
+    return workspace, _buf(workspace, "workspace", 0, device=device).value, \
         workspace.numel() * workspace.element_size()
 
 
@@ -176,7 +178,7 @@ def zero_linear(x, w, y, bias=None, act: int = ZERO_ACT_NONE, drop=None, residua
     py, ldy = _mat(y, "y", out, yt, dev)
     pr, ldr = (None, n) if residual is None else _mat(residual, "residual", out, yt, dev)
     pz, ldz = (None, n) if z is None else _mat(z, "z", out, dt, dev)
-    ws, nb = _scratch(ZERO_LINEAR, m, n, k, workspace, stream, x.device)
+    held, ws, nb = _scratch(ZERO_LINEAR, m, n, k, workspace, stream, x.device)
     _call(_lib.zero_linear, "zero_linear", dev, stream, px, _CODE[dt], ldx, pw, ldw,
           None if bias is None else _buf(bias, "bias", n, dt, x.device), m, n, k, act,
           None if drop is None else drop._c(x.device), pr, ldr, py, _CODE[yt], ldy, pz, ldz, ws,
@@ -198,7 +200,7 @@ def zero_linear_dgrad(dy, w, dx, act: int = ZERO_ACT_NONE, z=None, drop=None, re
     px, lddx = _mat(dx, "dx", out, xt, dev)
     pr, ldr = (None, k) if residual is None else _mat(residual, "residual", out, xt, dev)
     pz, ldz = (None, k) if z is None else _mat(z, "z", out, dt, dev)
-    ws, nb = _scratch(ZERO_LINEAR_DGRAD, m, n, k, workspace, stream, dy.device)
+    held, ws, nb = _scratch(ZERO_LINEAR_DGRAD, m, n, k, workspace, stream, dy.device)
     _call(_lib.zero_linear_dgrad, "zero_linear_dgrad", dev, stream, py, _CODE[dt], lddy, pw, ldw,
           m, n, k, act, pz, ldz, None if drop is None else drop._c(dy.device), pr, ldr, px,
           _CODE[xt], lddx, ws, nb)
@@ -216,7 +218,7 @@ def zero_linear_wgrad(dy, x, dw, db=None, accumulate: bool = False, stream=None,
     py, lddy = _mat(dy, "dy", (m, n), dt, dev)
     px, ldx = _mat(x, "x", (m, k), dt, dev)
     pg, lddw = _mat(dw, "dw", (n, k), gt, dev)
-    ws, nb = _scratch(ZERO_LINEAR_WGRAD, m, n, k, workspace, stream, dy.device)
+    held, ws, nb = _scratch(ZERO_LINEAR_WGRAD, m, n, k, workspace, stream, dy.device)
     _call(_lib.zero_linear_wgrad, "zero_linear_wgrad", dev, stream, py, _CODE[dt], lddy, px, ldx,
           m, n, k, pg, _CODE[gt], lddw,
           None if db is None else _buf(db, "db", n, gt, dy.device), int(bool(accumulate)), ws, nb)
