@@ -378,7 +378,11 @@ struct Stage {
 // read that row again (their outputs are never stored).  The instruction is
 // written out because the compiler makes every later read of shared memory
 // wait for all copies it knows of; the kernel waits for the ones it needs.
-// It has no output register, and its inputs are read when it issues.
+// It has no output register, and its inputs are read when it issues.  The
+// compiler writes m0 (the place in shared memory) but does not see that the
+// statement holds a memory instruction: the five wait states before it are
+// those after a vector write of the base's scalar registers (the way back of a
+// spilled one), and cover the one after m0's.
 template <bool KC, int ROWS, int THREADS, bool Q>
 struct Direct {
     static constexpr int N = ROWS * kBK / 8 / THREADS;
@@ -405,11 +409,11 @@ struct Direct {
     }
     // copy n of a step; tile: its byte address in shared memory
     __device__ __forceinline__ void issue(int n, uint32_t tile, int wave) const {
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+        asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                      :
-                     : "s"(tile + 2 * piece_at<KC, ROWS>(n * THREADS + wave * kWave)),
+                     : "{m0}"(tile + 2 * piece_at<KC, ROWS>(n * THREADS + wave * kWave)),
                        "v"(off[KC ? n : 0]), "s"(base + n * apart)
-                     : "memory", "m0");
+                     : "memory");
     }
     __device__ __forceinline__ void next() { base += stride; }
 };
