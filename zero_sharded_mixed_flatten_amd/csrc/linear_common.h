@@ -197,9 +197,13 @@ __device__ __forceinline__ f32x4 drop_apply(const Drop &d, u32x4 w, int half, f3
 
 // ---------------------------------------------------------------------------
 // activations (fp32).  Sigmoids are 1 / (1 + 2^(-u log2 e)) by the hardware's
-// exp2 and reciprocal, each good to about an ulp: a relative error of some
-// 2^-22, below the half step 2^-11 of the finest 16-bit output; with an fp32
-// output it is the largest error of the call.
+// exp2 and reciprocal, each good to about an ulp.  The argument's own
+// roundings weigh |u| in the falling tail: a relative error of
+// (6 |u| + 8) 2^-24 at most, 2^-17 at u = -20, below the half step 2^-11 of
+// the finest 16-bit output; with an fp32 output it is the largest error of
+// the call.  The erf GELU takes erfc, which keeps its relative error there
+// (1 + erf cancels: 4 % off at v = -5); its argument's roundings weigh v^2, a
+// relative error of (2 v^2 + 14) 2^-24.  A sigmoid below 2^-126 may be 0.
 
 // The epilogues are bound by these instructions (a 256 x 256 tile's outputs
 // wait for them alone), so the constants are folded and multiply-adds fused.
@@ -216,7 +220,7 @@ constexpr float kTanh1 = 1.5957691216057308f, kTanh3 = kTanh1 * 0.044715f;
 __device__ __forceinline__ float act_value(float v, int act) {
     switch (act) {
         case ZERO_ACT_RELU: return v > 0.0f ? v : (v != v ? v : 0.0f);
-        case ZERO_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+        case ZERO_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
         case ZERO_ACT_GELU_TANH:
             return v * logistic(v * __builtin_fmaf(-kLog2e * kTanh3, v * v, -kLog2e * kTanh1));
         case ZERO_ACT_SILU: return v * logistic(-kLog2e * v);
@@ -251,7 +255,7 @@ __device__ __forceinline__ float act_slope(float v, int act) {
     float s, t, d;
     switch (act) {
         case ZERO_ACT_GELU:
-            s = __builtin_fmaf(0.5f, erff(v * 0.70710678118654752f), 0.5f);
+            s = 0.5f * erfcf(v * -0.70710678118654752f);
             t = __builtin_amdgcn_exp2f(v * v * (-0.5f * kLog2e));
             d = v * 0.39894228040143268f;
             break;
