@@ -13,11 +13,11 @@
 // of one i: its outputs, residuals and biases are vectors.
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
 #include "linear_common.h"
+#include "linear_plan.h"
 
 namespace {
 
@@ -26,10 +26,6 @@ using namespace zero_linear_impl;
 
 using s16x4 = short __attribute__((ext_vector_type(4)));
 using s16x8 = short __attribute__((ext_vector_type(8)));
-
-constexpr int kBK = 64;  // contraction elements of one step
-
-enum Op { FWD = ZERO_LINEAR, DGRAD = ZERO_LINEAR_DGRAD, WGRAD = ZERO_LINEAR_WGRAD };
 
 struct Epilogue {
     const uint16_t *bias;
@@ -883,69 +879,10 @@ __global__ void __launch_bounds__(256) join_kernel(Args a) {
 // ---------------------------------------------------------------------------
 // host
 
-constexpr int kCUs = 256;
 constexpr int64_t kMaxTiles = int64_t(1) << 23;  // a launch has less than 2^32 threads
-
-struct Plan {
-    int bi, bj, parts;  // bi == 16 or 32: the kernel for few rows
-    int64_t chunk;
-};
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
-    if (op == FWD && ni <= 32 && nj < (int64_t(1) << 26))
-        return Plan{ni <= 16 ? 16 : 32, 16, 1, nc};
-    const int64_t steps = std::max<int64_t>(ceil_div(nc, kBK), 1);
-    // 256 x 256 tiles read least from shared memory and from memory a
-    // product, but one fills a CU.  They pay from five eighths of a round on
-    // and where the main loop outweighs the epilogue.  Times (us) with them
-    // and with 128 x 128 tiles, on inputs that change from call to call:
-    //   2500 x 4096 x 4096 (160 tiles)                 87 :  99
-    //   8192 x 6400 x 1600                            153 : 164
-    //   wgrad 6400 x 1600 over 8192 rows (175 tiles)  182 : 217
-    //   the same over 512 rows                       23.5 : 23.1
-    //   wgrad 4096 x 4096 over 512 rows (256 tiles)    29 :  34
-    //   wgrad 11008 x 4096 over 64 rows                52 :  50
-    //   256 x 50257 x 1600                             62 :  83
-    // and where they would hang further over the edges, the small ones:
-    //   333 x 50257 x 1600                            104 : 101
-    const int64_t large = ceil_div(ni, 256) * ceil_div(nj, 256);
-    const int64_t small = ceil_div(ni, 128) * ceil_div(nj, 128);
-    if (large >= kCUs * 5 / 8 && 4 * large * 7 <= small * 8 && steps > (large >= kCUs ? 4 : 8))
-        return Plan{256, 256, 1, steps * kBK};
-    Plan p{ni <= 64 ? 64 : 128, 128, 1, 0};
-    // Parts of the contraction, while all of them fit the card at once.  A
-    // step takes 0.62 us with one workgroup on a CU and 0.95 with two, and
-    // joining costs 4 us and 0.5 a part.  Undivided : divided as this says:
-    // 128 x 4096 x 4096 41 : 20 us (8 parts; 25 in 16), 64 x 4096 x 11008
-    // 124 : 29, wgrad 1600 x 1600 over 4096 rows 47 : 36; 512 x 6400 x 1600
-    // is left whole, 21 us (27 in 2).
-    const int64_t tiles = ceil_div(ni, p.bi) * ceil_div(nj, p.bj);
-    int64_t parts = 1;
-    double best = 0.0;
-    for (int64_t n = 1; n <= 64 && n <= steps && (n == 1 || tiles * n <= 2 * kCUs); ++n) {
-        const double cost = static_cast<double>(ceil_div(steps, n)) * (tiles * n <= kCUs ? 0.62 : 0.95) +
-                            (n == 1 ? 0.0 : 4.0 + 0.5 * static_cast<double>(n));
-        if (n == 1 || cost < best) {
-            best = cost;
-            parts = n;
-        }
-    }
-    p.chunk = ceil_div(steps, parts) * kBK;
-    p.parts = static_cast<int>(std::max<int64_t>(1, ceil_div(nc, p.chunk)));
-    return p;
-}
 
 int64_t partial_bytes(const Plan &p, int64_t ni, int64_t nj) {
     return p.parts == 1 ? 0 : p.parts * ni * (padded4(nj) + 1) * 4 + 16;
-}
-
-// Direct copies move 16-byte pieces: every row 16-byte aligned, and (rows of
-// lanes) a whole number of pieces long; a tile's rows span less than 2^32
-// bytes.
-bool direct_ok(const uint16_t *p, int64_t ld, int64_t lanes) {
-    return aligned16(p) && ld % 8 == 0 && lanes % 8 == 0 && ld < (int64_t(1) << 22);
 }
 
 template <int OP, class T, int BI, int BJ, int WI, int WJ, bool DIRECT>
@@ -965,10 +902,8 @@ zero_status run_tiles(Args &a, hipStream_t st) {
     a.quarter = -1;
     const int64_t tiles = static_cast<int64_t>(a.tiles_i) * a.tiles_j;
     if (tiles >= kMaxTiles) return ZERO_EINVAL;
-    // One of the largest tiles occupies a CU.  What is left after the last
-    // whole round of them, up to half a round, runs as quarters, two to a CU.
-    const int64_t rest = tiles % kCUs;
-    if (BI == 256 && tiles > kCUs && rest > 0 && rest <= kCUs / 2) {
+    const int64_t rest = BI == 256 ? quartered(tiles) : 0;
+    if (rest > 0) {
         run_grid<OP, T, BI, BJ, WI, WJ, DIRECT>(a, tiles - rest, st);
         a.quarter = static_cast<int32_t>(tiles - rest);
         run_grid<OP, T, 128, 128, 2, 2, DIRECT>(a, 4 * rest, st);
