@@ -22,8 +22,8 @@
  *  - A matrix occupies its span, from its first element to one past its last:
  *    two matrices that interleave (column ranges of one buffer) overlap.
  *  - Dimensions are 0 <= m, n, k <= 2^31 - 1024, a matrix spans at most 2^60
- *    elements, and a product has less than 2^23 output tiles of 64 x 128.  An empty output is a no-op; an empty contraction gives
- *    sums of zero.
+ *    elements, and a product has less than 2^23 output tiles of 64 x 128.  An
+ *    empty output is a no-op; an empty contraction gives sums of zero.
  *  - Products of 16-bit elements are exact in fp32 and are summed in fp32 by
  *    the matrix instructions; bias, activation, dropout and residual are
  *    fp32, and each output is rounded once, to nearest even.  The order of a
@@ -66,8 +66,12 @@ typedef enum zero_act {
  * is a device int64 read when the kernel runs, for instance the counter that
  * zero_step_counter_advance moves, so that a captured graph draws a new mask
  * at every replay.  row0 places a call's rows in a longer batch: a batch
- * split over calls by rows draws the mask of one call.  Calls that should
- * draw independent masks take different offsets (or seeds). */
+ * split over calls by rows draws the mask of one call.
+ * Under one seed, two calls whose streams (offset + *step) are equal draw the
+ * same mask: a layer and its backward pass on purpose, but a layer at offset 1
+ * in step 5 also that of a layer at offset 0 in step 6.  Calls that should
+ * draw independent masks take different seeds, or offsets that the step
+ * counter never bridges: multiples of 2^32 serve 2^32 steps. */
 typedef struct zero_dropout_params {
     double p;            /* in [0, 1) */
     uint64_t seed;

@@ -33,7 +33,11 @@ class _DropoutParams(ctypes.Structure):
 class ZeroDropout:
     """Dropout D: the mask is a function of seed, offset (+ *step, an int64
     GPU tensor such as new_step_counter()'s, read when the kernel runs), row
-    (counted from row0) and column; see zero_linear.h for the exact bits."""
+    (counted from row0) and column; see zero_linear.h for the exact bits.
+    Calls of one seed whose offset + *step are equal draw the same mask, those
+    left at the defaults too: layers that should not share one take seeds of
+    their own, or offsets that the counter never bridges (layer << 32 serves
+    2^32 steps)."""
     p: float
     seed: int = 0
     offset: int = 0
