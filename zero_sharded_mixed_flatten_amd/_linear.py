@@ -9,6 +9,12 @@
 Matrices are 2-D tensors or views whose rows are contiguous; any row stride
 and any element alignment is taken.  Dimensions come from the tensors and are
 checked against each other before anything is launched.
+
+As everywhere in the binding the calls read and write through plain addresses:
+autograd records none of them, whatever requires_grad says, and a tensor's
+version counter does not move when a call writes into it, so autograd does not
+notice if it had saved that tensor.  The backward pass is the caller's own
+zero_linear_dgrad, zero_linear_wgrad and zero_dropout.
 """
 import ctypes
 from dataclasses import dataclass
