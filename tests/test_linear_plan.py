@@ -102,3 +102,16 @@ def test_parts_cover_the_contraction_once(plan):
             assert p.bi <= 128 and p.tiles * p.parts <= 512
         if p.bi <= 32:
             assert op == "linear" and m <= 32 and p.parts == 1
+
+
+def test_few_rows(plan):
+    """the few-rows kernel up to 16 rows; from 17 on only where no CU has more
+    than 6400 of the contraction to do"""
+    for m, n, k in [(1, 48, 12288), (16, 50257, 1600), (16, 4096, 11008), (17, 1600, 1600),
+                    (32, 4096, 4096), (32, 4096, 6400), (32, 6400, 2048), (32, 2000, 200)]:
+        p = plan("linear", m, n, k)
+        assert (p.bi, p.parts) == (16 if m <= 16 else 32, 1)
+    for m, n, k in [(32, 48, 12288), (17, 1024, 12288), (32, 4096, 11008), (32, 11008, 4096),
+                    (24, 32000, 2048), (32, 6400, 6400)]:
+        p = plan("linear", m, n, k)
+        assert p.bi == 64

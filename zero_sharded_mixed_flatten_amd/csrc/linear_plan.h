@@ -23,7 +23,25 @@ struct Plan {
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 inline Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
-    if (op == FWD && ni <= 32 && nj < (int64_t(1) << 26))
+    // Few rows: 16 columns a workgroup, the contraction undivided, against 64 x
+    // 128 tiles in parts.  Up to 16 rows the former wins nearly everywhere; from
+    // 17 on it multiplies twice for every piece of W, and loses where each CU
+    // has much to do alone.  Times (us) few rows : tiles, W from HBM, for 1, 16
+    // and 32 rows (24 and more are like 32):
+    //   1600 x 1600    4.8 : 11.4     5.9 : 11.8     7.7 : 11.9
+    //   4096 x 4096    9.9 : 18.3*   11.6 : 18.4    15.0 : 18.4
+    //   1600 x 6400   10.2 : 17.5    13.9 : 18.0    19.9 : 18.1
+    //   4096 x 6400   12.4 : 23.3    17.6 : 23.5    21.7 : 23.4
+    //   11008 x 4096  23.1 : 26.4*   27.0 : 26.5    37.5 : 27.2
+    //   32000 x 6400    87 :   83*    107 :   85     148 :   88
+    //   1024 x 12288  16.4 : 21.2    23.8 : 22.3    35.0 : 22.5
+    //   48 x 12288    15.1 : 16.7    22.8 : 16.0    33.3 : 16.2
+    // (* 8 rows).  With W at an odd element both are slower, the former more:
+    //   16 rows, 1600 x 2048 11.3 : 14.4, 4096 x 6400 31 : 29, 6400 x 6400 58 : 32
+    // which the rule leaves out, since a product's workspace depends on its
+    // sizes only.
+    if (op == FWD && ni <= 32 && nj < (int64_t(1) << 26) &&
+        (ni <= 16 || ceil_div(nj, 16 * kCUs) * nc <= 6400))
         return Plan{ni <= 16 ? 16 : 32, 16, 1, nc};
     const int64_t steps = std::max<int64_t>(ceil_div(nc, kBK), 1);
     // 256 x 256 tiles read least from shared memory and from memory a
