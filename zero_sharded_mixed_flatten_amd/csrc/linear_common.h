@@ -15,8 +15,6 @@
 namespace zero_linear_impl {
 
 using f32x4 = float __attribute__((ext_vector_type(4)));
-using f32x2 = float __attribute__((ext_vector_type(2)));
-using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 using u16x4 = uint16_t __attribute__((ext_vector_type(4)));
 
@@ -24,7 +22,6 @@ using u16x4 = uint16_t __attribute__((ext_vector_type(4)));
 // 16-bit element types
 
 struct BF16 {
-    using elem = __bf16;
     static __device__ __forceinline__ float up(uint16_t h) {
         return __builtin_bit_cast(float, static_cast<uint32_t>(h) << 16);
     }
@@ -33,7 +30,6 @@ struct BF16 {
     }
 };
 struct FP16 {
-    using elem = _Float16;
     static __device__ __forceinline__ float up(uint16_t h) {
         return static_cast<float>(__builtin_bit_cast(_Float16, h));
     }
