@@ -48,15 +48,17 @@ inline Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
     // product, but one fills a CU.  They pay from five eighths of a round on
     // and where the main loop outweighs the epilogue.  Times (us) with them
     // and with 128 x 128 tiles, on inputs that change from call to call:
-    //   2500 x 4096 x 4096 (160 tiles)                 87 :  99
-    //   8192 x 6400 x 1600                            153 : 164
-    //   wgrad 6400 x 1600 over 8192 rows (175 tiles)  182 : 217
-    //   the same over 512 rows                       23.5 : 23.1
-    //   wgrad 4096 x 4096 over 512 rows (256 tiles)    29 :  34
-    //   wgrad 11008 x 4096 over 64 rows                52 :  50
-    //   256 x 50257 x 1600                             62 :  83
+    //   2500 x 4096 x 4096 (160 tiles)                 76 :  96
+    //   8192 x 6400 x 1600                            152 : 162
+    //   wgrad 6400 x 1600 over 8192 rows (175 tiles)  181 : 221
+    //   the same over 512 rows                       22.1 : 23.1
+    //   wgrad 4096 x 4096 over 512 rows (256 tiles)  27.8 : 31.6
+    //   wgrad 11008 x 4096 over 64 rows                47 :  39
+    //   256 x 50257 x 1600                             62 :  82
     // and where they would hang further over the edges, the small ones:
-    //   333 x 50257 x 1600                            104 : 101
+    //   333 x 50257 x 1600                            105 : 100
+    // Operands that cannot be copied directly (direct_ok below) run as 128 x
+    // 128 in one part where the large tiles are chosen here.
     const int64_t large = ceil_div(ni, 256) * ceil_div(nj, 256);
     const int64_t small = ceil_div(ni, 128) * ceil_div(nj, 128);
     if (large >= kCUs * 5 / 8 && 4 * large * 7 <= small * 8 && steps > (large >= kCUs ? 4 : 8))
@@ -65,9 +67,9 @@ inline Plan plan_for(int op, int64_t ni, int64_t nj, int64_t nc) {
     // Parts of the contraction, while all of them fit the card at once.  A
     // step takes 0.62 us with one workgroup on a CU and 0.95 with two, and
     // joining costs 4 us and 0.5 a part.  Undivided : divided as this says:
-    // 128 x 4096 x 4096 41 : 20 us (8 parts; 25 in 16), 64 x 4096 x 11008
-    // 124 : 29, wgrad 1600 x 1600 over 4096 rows 47 : 36; 512 x 6400 x 1600
-    // is left whole, 21 us (27 in 2).
+    // 128 x 4096 x 4096 41 : 19.5 us (8 parts; 24 in 16), 64 x 4096 x 11008
+    // 122 : 29, wgrad 1600 x 1600 over 4096 rows 46 : 36; 512 x 6400 x 1600
+    // is left whole, 20 us (25 in 2).
     const int64_t tiles = ceil_div(ni, p.bi) * ceil_div(nj, p.bj);
     int64_t parts = 1;
     double best = 0.0;
