@@ -471,7 +471,7 @@ __device__ __forceinline__ void tile_of(const Args &a, int b, int &ti, int &tj) 
 // largest tiles has a block of 128 x 64, two waves a SIMD (128 x 128 would
 // read less but does not fit the registers).  Measured at 8192 x 4096 x 11008
 // with mask and residual (555 us, 1.33 PFLOP/s): the matrix units are busy for
-// 60 to 66 % of the cycles, waves wait for 38 % of theirs (3 % on shared
+// 60 to 68 % of the cycles, waves wait for 36 to 38 % of theirs (3 % on shared
 // memory), memory delivers 2 TB/s, and after some launches on end the clock
 // inside this loop falls from 2.2 to 1.9 GHz.
 template <int OP, class T, int BI, int BJ, int WI, int WJ, bool DIRECT, bool DB>
@@ -778,8 +778,8 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
 // operand is 16 contiguous bytes of a row of W), the next chunk's loads under
 // way while one is multiplied.  The waves' sums are added in their order in
 // shared memory: one launch, no workspace.  Rows past the last repeat it;
-// their outputs are not stored.  One row: 6400 x 1600 6 us (3.4 TB/s), 4096 x
-// 6400 12.4 (4.2 TB/s), 1600 x 6400 10.2 (2.0 TB/s).
+// their outputs are not stored.  One row: 6400 x 1600 7.4 us (2.8 TB/s), 4096 x
+// 6400 12.5 (4.2 TB/s), 1600 x 6400 10.2 (2.0 TB/s).
 constexpr int kSkinnyWaves = 8, kSkinnyChunk = 128;
 
 template <class T, int R>
