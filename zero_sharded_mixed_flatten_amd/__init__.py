@@ -2,8 +2,9 @@
 mixed-precision optimizer step on MI355X (gfx950).
 
 A thin ctypes binding over libzero_shard.so (include/zero_shard.h; the layer
-products of include/zero_linear.h in _linear.py).  Every
-function here has the name of the C entry point it calls and only marshals
+products of include/zero_linear.h in _linear.py, the layer norm of
+include/zero_norm.h in _norm.py, the Muon step of include/zero_muon.h in
+_muon.py).  Every function here has the name of the C entry point it calls and only marshals
 arguments: torch tensors become device pointers and dtype codes, the current
 torch stream becomes the HIP stream.  All work runs in the library's HIP
 kernels; there is no fallback of any kind -- importing this package without
@@ -842,6 +843,11 @@ from ._linear import (  # noqa: E402  (the second header's part of the binding)
     ZERO_ACT_GELU, ZERO_ACT_GELU_TANH, ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_SILU, ZERO_LINEAR,
     ZERO_LINEAR_DGRAD, ZERO_LINEAR_WGRAD, ZeroDropout, zero_dropout, zero_linear,
     zero_linear_dgrad, zero_linear_wgrad, zero_linear_workspace_bytes)
+from ._norm import (  # noqa: E402
+    zero_layernorm, zero_layernorm_backward, zero_layernorm_workspace_bytes)
+from ._muon import (  # noqa: E402
+    ZERO_NS_MAX_STEPS, zero_muon_momentum, zero_muon_momentum_dc, zero_muon_update,
+    zero_muon_update_dc, zero_orthogonalize, zero_orthogonalize_workspace_bytes)
 
 __all__ = ["zero_flatten_layout", "zero_shard_segments", "zero_dim0_layout", "zero_dim0_segments", "zero_shard_reduce",
            "zero_shard_adamw", "zero_shard_adamw_ex", "zero_loss_scale_update",
@@ -852,4 +858,7 @@ __all__ = ["zero_flatten_layout", "zero_shard_segments", "zero_dim0_layout", "ze
            "zero_linear", "zero_linear_dgrad", "zero_linear_wgrad", "zero_dropout",
            "zero_linear_workspace_bytes", "ZeroDropout", "ZERO_LINEAR", "ZERO_LINEAR_DGRAD",
            "ZERO_LINEAR_WGRAD", "ZERO_ACT_NONE", "ZERO_ACT_RELU", "ZERO_ACT_GELU",
-           "ZERO_ACT_GELU_TANH", "ZERO_ACT_SILU"]
+           "ZERO_ACT_GELU_TANH", "ZERO_ACT_SILU", "zero_layernorm", "zero_layernorm_backward",
+           "zero_layernorm_workspace_bytes", "zero_muon_momentum", "zero_muon_momentum_dc",
+           "zero_muon_update", "zero_muon_update_dc", "zero_orthogonalize",
+           "zero_orthogonalize_workspace_bytes", "ZERO_NS_MAX_STEPS"]

@@ -140,13 +140,18 @@ def zero_linear_workspace_bytes(op: int, m: int, n: int, k: int) -> int:
 
 
 def _scratch(op, m, n, k, workspace, stream, device):
-    """(tensor, address, bytes) of the product's workspace: the caller's, or a
-    new one allocated on the call's stream.  The caller holds the tensor until
-    its kernels are enqueued: freed after that, its block is reused in the
+    """_scratch_of the product's workspace"""
+    return _scratch_of(0 if workspace is not None else
+                       _lib.zero_linear_workspace_bytes(op, m, n, k), workspace, stream, device)
+
+
+def _scratch_of(need, workspace, stream, device):
+    """(tensor, address, bytes) of a call's workspace: the caller's, or a new
+    one of `need` bytes allocated on the call's stream.  The caller holds the
+    tensor until its kernels are enqueued: freed after that, its block is reused in the
     stream's order, behind them; freed before, another thread could be handed
     it first (the library is called without the interpreter's lock)."""
     if workspace is None:
-        need = _lib.zero_linear_workspace_bytes(op, m, n, k)
         if need <= 0:
             return None, None, 0
         with torch.cuda.stream(_torch_stream(stream, device)):

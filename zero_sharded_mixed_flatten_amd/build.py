@@ -16,7 +16,8 @@ LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libzero_shard.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("zero_shard.hip", "quant8.hip", "flat_copy.hip",
-                                                   "linear.hip", "dropout.hip", "layout.cpp")]
+                                                   "linear.hip", "dropout.hip", "norm.hip",
+                                                   "muon.hip", "orthogonalize.hip", "layout.cpp")]
 
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -25,8 +26,7 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
 
 def build(verbose: bool = False) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
-    # only the entry points of include/zero_shard.h and include/zero_linear.h
-    # are exported
+    # only the entry points of the headers in include/ are exported
     cmd = [HIPCC] + FLAGS + ["-I", os.path.join(ROOT, "include"),
                              "-o", LIB + ".tmp"] + SOURCES
     if verbose:

@@ -1,0 +1,344 @@
+// muon.hip -- gfx950 kernels of the elementwise parts of the Muon step:
+// zero_muon_momentum and zero_muon_update.  Streaming passes over a range of
+// the shard, four elements a lane, every load issued before the arithmetic;
+// HBM bounds both.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "step_common.h"
+#include "zero_muon.h"
+
+namespace {
+
+using namespace zero_host;
+using namespace zero_step;
+
+struct Control {
+    const uint32_t *skip;
+    const double *sumsq;
+    double max_norm;
+    const zero_loss_scale *loss_scale;
+    double grad_scale;
+    const zero_step_consts *dc;
+};
+
+// The step's constants and clip coefficient, the same in every thread; false
+// where the step writes nothing.
+__device__ __forceinline__ bool resolve(Control k, Consts &c, float &clip) {
+    if (k.skip != nullptr && *k.skip != 0u) return false;
+    if (k.dc != nullptr) {
+        c = consts_of(*k.dc);
+        if (step_held(c)) return false;
+        k.grad_scale = k.dc->grad_scale;
+    }
+    if (k.loss_scale != nullptr)
+        c.s = static_cast<float>(k.grad_scale / static_cast<double>(k.loss_scale->scale));
+    clip = 1.0f;
+    if (k.sumsq != nullptr && k.max_norm > 0.0) {
+        const double norm = sqrt(*k.sumsq) * static_cast<double>(c.s);
+        const double cc = k.max_norm / (norm + 1e-6);
+        if (cc < 1.0) clip = static_cast<float>(cc);
+    }
+    return true;
+}
+
+// four elements at any alignment (global memory takes it), n < 4 of them one
+// by one; fp32, or 16-bit as pairs
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+template <int DT>
+__device__ __forceinline__ typename GradT<DT>::quad quad_at(const typename GradT<DT>::elem *p,
+                                                            int n) {
+    if (n >= kQuad) {
+        if constexpr (DT == ZERO_FP32)
+            return __builtin_nontemporal_load(reinterpret_cast<const f32x4_any *>(p));
+        else
+            return __builtin_nontemporal_load(reinterpret_cast<const u32x2_any *>(p));
+    }
+    if constexpr (DT == ZERO_FP32) {
+        return f32x4{p[0], n > 1 ? p[1] : 0.0f, n > 2 ? p[2] : 0.0f, 0.0f};
+    } else {
+        const uint32_t b = n > 1 ? p[1] : 0u, c = n > 2 ? p[2] : 0u;
+        return u32x2{p[0] | b << 16, c};
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void quad_to(typename GradT<DT>::elem *p, const float (&v)[kQuad],
+                                        int n) {
+    if constexpr (DT == ZERO_FP32) {
+        if (n >= kQuad) {
+            store16(p, f32x4{v[0], v[1], v[2], v[3]});
+        } else {
+#pragma unroll
+            for (int e = 0; e < kQuad - 1; ++e)
+                if (e < n) p[e] = v[e];
+        }
+    } else {
+        float r[kQuad];
+#pragma unroll
+        for (int e = 0; e < kQuad; ++e) r[e] = as_rounded_f32(v[e]);
+        if (n >= kQuad) {
+            store8(p, u32x2{narrow2<DT>(r[0], r[1]), narrow2<DT>(r[2], r[3])});
+        } else {
+#pragma unroll
+            for (int e = 0; e < kQuad - 1; ++e)
+                if (e < n) p[e] = narrow1<DT>(r[e]);
+        }
+    }
+}
+
+// rows fetched together where their number is not a compile-time one
+constexpr int kBatch = 8;
+
+template <int GDT, int UDT, int NDP>
+__global__ void __launch_bounds__(kWave)
+momentum_kernel(const typename GradT<GDT>::elem *__restrict__ g, int64_t ld, int n_rows,
+                int64_t len, float *__restrict__ mom, typename GradT<UDT>::elem *__restrict__ u,
+                int nesterov, Consts c, Control ctl) {
+    float clip;
+    if (!resolve(ctl, c, clip)) return;
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kWave + threadIdx.x) * kQuad;
+    if (at >= len) return;
+    const int n = static_cast<int>(min(len - at, static_cast<int64_t>(kQuad)));
+    const typename GradT<GDT>::elem *p = g + at;
+    constexpr int B = NDP > 0 ? NDP : kBatch;
+    typename GradT<GDT>::quad x[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k)
+        if (NDP > 0 || k < n_rows) x[k] = quad_at<GDT>(p + k * ld, n);
+    const f32x4 old = quad_at<ZERO_FP32>(mom + at, n);
+    loads_issued();
+    float a[kQuad], t[kQuad];
+    widen_quad<GDT>(a, x[0]);
+#pragma unroll
+    for (int k = 1; k < B; ++k)
+        if (NDP > 0 || k < n_rows) {
+            widen_quad<GDT>(t, x[k]);
+#pragma unroll
+            for (int e = 0; e < kQuad; ++e) a[e] = a[e] + t[e];
+        }
+    if constexpr (NDP == 0) {
+        for (int k0 = B; k0 < n_rows; k0 += B) {
+#pragma unroll
+            for (int k = 0; k < B; ++k)
+                if (k0 + k < n_rows) x[k] = quad_at<GDT>(p + (k0 + k) * ld, n);
+            loads_issued();
+#pragma unroll
+            for (int k = 0; k < B; ++k)
+                if (k0 + k < n_rows) {
+                    widen_quad<GDT>(t, x[k]);
+#pragma unroll
+                    for (int e = 0; e < kQuad; ++e) a[e] = a[e] + t[e];
+                }
+        }
+    }
+    float m[kQuad], v[kQuad];
+#pragma unroll
+    for (int e = 0; e < kQuad; ++e) {
+        float ge = a[e] * c.s;
+        if (clip < 1.0f) ge = ge * clip;
+        m[e] = c.b1 * old[e] + ge;
+        v[e] = nesterov ? ge + c.b1 * m[e] : m[e];
+    }
+    quad_to<ZERO_FP32>(mom + at, m, n);
+    quad_to<UDT>(u + at, v, n);
+}
+
+template <int ODT, int WDT>
+__global__ void __launch_bounds__(kWave)
+update_kernel(const uint16_t *__restrict__ o, int64_t len, float *__restrict__ W,
+              uint16_t *__restrict__ slot, float k, Consts c, Control ctl) {
+    float clip;
+    if (!resolve(ctl, c, clip)) return;
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kWave + threadIdx.x) * kQuad;
+    if (at >= len) return;
+    const int n = static_cast<int>(min(len - at, static_cast<int64_t>(kQuad)));
+    const u32x2 ov = quad_at<ODT>(o + at, n);
+    const f32x4 old = quad_at<ZERO_FP32>(W + at, n);
+    loads_issued();
+    float t[kQuad], w[kQuad];
+    widen_quad<ODT>(t, ov);
+#pragma unroll
+    for (int e = 0; e < kQuad; ++e) w[e] = old[e] * c.d - c.lr * (k * t[e]);
+    quad_to<ZERO_FP32>(W + at, w, n);
+    quad_to<WDT>(slot + at, w, n);
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+inline int64_t bytes_of(zero_dtype t) { return t == ZERO_FP32 ? 4 : 2; }
+inline bool aligned_to(const void *p, int64_t b) {
+    return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(b) == 0;
+}
+
+template <class F>
+void for_launches(int64_t len, F f) {
+    for (int64_t at = 0; at < len; at += kLaunchElems) f(at, std::min(kLaunchElems, len - at));
+}
+inline uint32_t groups_of(int64_t len) {
+    return static_cast<uint32_t>((len + kWave * kQuad - 1) / (kWave * kQuad));
+}
+
+template <int GDT, int UDT, int NDP>
+void run_momentum(const void *grads, int64_t ld, int32_t n_rows, int64_t len, float *mom, void *u,
+                  int32_t nesterov, const Consts &c, const Control &k, hipStream_t st) {
+    const auto *g = static_cast<const typename GradT<GDT>::elem *>(grads);
+    auto *out = static_cast<typename GradT<UDT>::elem *>(u);
+    for_launches(len, [&](int64_t at, int64_t n) {
+        momentum_kernel<GDT, UDT, NDP><<<groups_of(n), kWave, 0, st>>>(
+            g + at, ld, n_rows, n, mom + at, out + at, nesterov != 0, c, k);
+    });
+}
+
+template <int GDT, int UDT>
+void momentum_rows(const void *grads, int64_t ld, int32_t n_rows, int64_t len, float *mom, void *u,
+                   int32_t nesterov, const Consts &c, const Control &k, hipStream_t st) {
+    switch (n_rows) {
+        case 1: run_momentum<GDT, UDT, 1>(grads, ld, n_rows, len, mom, u, nesterov, c, k, st); break;
+        case 8: run_momentum<GDT, UDT, 8>(grads, ld, n_rows, len, mom, u, nesterov, c, k, st); break;
+        default: run_momentum<GDT, UDT, 0>(grads, ld, n_rows, len, mom, u, nesterov, c, k, st);
+    }
+}
+
+template <int GDT>
+void momentum_types(const void *grads, int64_t ld, int32_t n_rows, int64_t len, float *mom,
+                    void *u, zero_dtype udt, int32_t nesterov, const Consts &c, const Control &k,
+                    hipStream_t st) {
+    if (udt == ZERO_BF16)
+        momentum_rows<GDT, ZERO_BF16>(grads, ld, n_rows, len, mom, u, nesterov, c, k, st);
+    else if (udt == ZERO_FP16)
+        momentum_rows<GDT, ZERO_FP16>(grads, ld, n_rows, len, mom, u, nesterov, c, k, st);
+    else
+        momentum_rows<GDT, ZERO_FP32>(grads, ld, n_rows, len, mom, u, nesterov, c, k, st);
+}
+
+zero_status momentum_impl(const void *grads, zero_dtype gdt, int32_t n_rows, int64_t ld,
+                          int64_t len, float *mom, void *u, zero_dtype udt, int32_t nesterov,
+                          const zero_adamw_hparams *hp, const zero_step_consts *dc,
+                          const zero_step_control *ctl, void *stream) {
+    for (zero_dtype t : {gdt, udt})
+        if (!dtype_ok(t) && t != ZERO_FP32) return ZERO_EINVAL;
+    if (!(dc ? aligned8(dc) : hparams_ok(hp))) return ZERO_EINVAL;
+    if (!rows_ok(n_rows, ld, len) || len > kMaxLen) return ZERO_EINVAL;
+    if (ctl && !std::isfinite(ctl->max_norm)) return ZERO_EINVAL;
+    if (len == 0) return ZERO_OK;
+    const int64_t ge = bytes_of(gdt), ue = bytes_of(udt);
+    if (!grads || !mom || !u || !aligned_to(grads, ge) || !aligned_to(mom, 4) ||
+        !aligned_to(u, ue))
+        return ZERO_EINVAL;
+    const Span sm = span_of(mom, len, 4), su = span_of(u, len, ue);
+    if (overlap(sm, su)) return ZERO_EALIAS;
+    for (int32_t k = 0; k < n_rows; ++k) {
+        const Span r = span_of(static_cast<const char *>(grads) + k * ld * ge, len, ge);
+        if (overlap(sm, r) || overlap(su, r)) return ZERO_EALIAS;
+    }
+    Control k{};
+    if (ctl) k = Control{ctl->skip, ctl->sumsq, ctl->max_norm, ctl->loss_scale, 0.0, nullptr};
+    k.grad_scale = dc ? 0.0 : hp->grad_scale;
+    k.dc = dc;
+    for (const Span &r : {span_of(dc, dc ? 1 : 0, sizeof(zero_step_consts)),
+                          span_of(k.skip, k.skip ? 1 : 0, 4), span_of(k.sumsq, k.sumsq ? 1 : 0, 8),
+                          span_of(k.loss_scale, k.loss_scale ? 1 : 0, sizeof(zero_loss_scale))})
+        if (overlap(sm, r) || overlap(su, r)) return ZERO_EALIAS;
+    const Consts c = dc ? Consts{} : make_consts(*hp);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (gdt == ZERO_BF16)
+        momentum_types<ZERO_BF16>(grads, ld, n_rows, len, mom, u, udt, nesterov, c, k, st);
+    else if (gdt == ZERO_FP16)
+        momentum_types<ZERO_FP16>(grads, ld, n_rows, len, mom, u, udt, nesterov, c, k, st);
+    else
+        momentum_types<ZERO_FP32>(grads, ld, n_rows, len, mom, u, udt, nesterov, c, k, st);
+    return launch_status();
+}
+
+template <int ODT, int WDT>
+void run_update(const uint16_t *o, int64_t len, float *w, uint16_t *slot, float scale,
+                const Consts &c, const Control &k, hipStream_t st) {
+    for_launches(len, [&](int64_t at, int64_t n) {
+        update_kernel<ODT, WDT>
+            <<<groups_of(n), kWave, 0, st>>>(o + at, n, w + at, slot + at, scale, c, k);
+    });
+}
+
+zero_status update_impl(const void *o, zero_dtype odt, float *master, void *weight_full,
+                        zero_dtype wdt, const zero_layout *layout, int32_t rank,
+                        int64_t shard_off, int64_t len, const zero_adamw_hparams *hp,
+                        const zero_step_consts *dc, double update_scale, const uint32_t *skip,
+                        void *stream) {
+    if (!dtype_ok(odt) || !dtype_ok(wdt) || !layout_ok(layout)) return ZERO_EINVAL;
+    if (!(dc ? aligned8(dc) : hparams_ok(hp)) || !std::isfinite(update_scale)) return ZERO_EINVAL;
+    if (rank < 0 || rank >= layout->n_dp || shard_off < 0 || len < 0 || len > kMaxLen)
+        return ZERO_EINVAL;
+    if (shard_off > layout->shard || len > layout->shard - shard_off) return ZERO_ERANGE;
+    if (len == 0) return ZERO_OK;
+    if (!o || !master || !weight_full || !aligned_to(o, 2) || !aligned_to(master, 4) ||
+        !aligned_to(weight_full, 2))
+        return ZERO_EINVAL;
+    uint16_t *slot = static_cast<uint16_t *>(weight_full) +
+                     static_cast<int64_t>(rank) * layout->shard + shard_off;
+    const Span sw = span_of(master, len, 4), ss = span_of(slot, len, 2);
+    if (overlap(sw, ss)) return ZERO_EALIAS;
+    for (const Span &r : {span_of(o, len, 2), span_of(dc, dc ? 1 : 0, sizeof(zero_step_consts)),
+                          span_of(skip, skip ? 1 : 0, 4)})
+        if (overlap(sw, r) || overlap(ss, r)) return ZERO_EALIAS;
+    const Consts c = dc ? Consts{} : make_consts(*hp);
+    const Control k{skip, nullptr, 0.0, nullptr, 0.0, dc};
+    const float scale = static_cast<float>(update_scale);
+    const auto *in = static_cast<const uint16_t *>(o);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (odt == ZERO_BF16)
+        wdt == ZERO_BF16
+            ? run_update<ZERO_BF16, ZERO_BF16>(in, len, master, slot, scale, c, k, st)
+            : run_update<ZERO_BF16, ZERO_FP16>(in, len, master, slot, scale, c, k, st);
+    else
+        wdt == ZERO_BF16
+            ? run_update<ZERO_FP16, ZERO_BF16>(in, len, master, slot, scale, c, k, st)
+            : run_update<ZERO_FP16, ZERO_FP16>(in, len, master, slot, scale, c, k, st);
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+zero_status zero_muon_momentum(const void *grads, zero_dtype gdt, int32_t n_rows, int64_t ld,
+                               int64_t len, float *mom, void *u, zero_dtype udt, int32_t nesterov,
+                               const zero_adamw_hparams *hp, const zero_step_control *ctl,
+                               void *stream) {
+    return momentum_impl(grads, gdt, n_rows, ld, len, mom, u, udt, nesterov, hp, nullptr, ctl,
+                         stream);
+}
+
+zero_status zero_muon_momentum_dc(const void *grads, zero_dtype gdt, int32_t n_rows, int64_t ld,
+                                  int64_t len, float *mom, void *u, zero_dtype udt,
+                                  int32_t nesterov, const zero_step_consts *consts,
+                                  const zero_step_control *ctl, void *stream) {
+    if (!consts) return ZERO_EINVAL;
+    return momentum_impl(grads, gdt, n_rows, ld, len, mom, u, udt, nesterov, nullptr, consts, ctl,
+                         stream);
+}
+
+zero_status zero_muon_update(const void *o, zero_dtype odt, float *master, void *weight_full,
+                             zero_dtype wdt, const zero_layout *layout, int32_t rank,
+                             int64_t shard_off, int64_t len, const zero_adamw_hparams *hp,
+                             double update_scale, const uint32_t *skip, void *stream) {
+    return update_impl(o, odt, master, weight_full, wdt, layout, rank, shard_off, len, hp, nullptr,
+                       update_scale, skip, stream);
+}
+
+zero_status zero_muon_update_dc(const void *o, zero_dtype odt, float *master, void *weight_full,
+                                zero_dtype wdt, const zero_layout *layout, int32_t rank,
+                                int64_t shard_off, int64_t len, const zero_step_consts *consts,
+                                double update_scale, const uint32_t *skip, void *stream) {
+    if (!consts) return ZERO_EINVAL;
+    return update_impl(o, odt, master, weight_full, wdt, layout, rank, shard_off, len, nullptr,
+                       consts, update_scale, skip, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,616 @@
+// orthogonalize.hip -- gfx950 kernels of zero_orthogonalize.
+//
+// Each matrix is worked on with its shorter side first, X [r][c], r <= c, laid
+// out in the workspace with both sides padded by zeros to multiples of 64, so
+// that every operand of every product is copied straight to shared memory.  A
+// round is three products on the matrix units:
+//   gram    A = X X^T                    (symmetric)
+//   square  P = a + b A + c A A          (symmetric)
+//   apply   X = P X
+// Rounding.  fp16 keeps 11 bits where bf16 keeps 8, at the same rate; every
+// value here is scaled by 2^12, which leaves room up to 16 above and down to
+// 2^-26 below at full precision.  Rounding A, P or X as a whole would cost a
+// few times 2^-11 of the result where singular values are alike, and all of
+// its small singular directions where they are not, since those are what the
+// rounds amplify.  So the diagonals, where the large part of A and P lies, are
+// kept apart in fp32 and enter as row factors in fp32:
+//   A = D + O:  A A = O O + (d_i + d_j) O_ij + (d_i^2 on the diagonal)
+//   P = E + Q:  P X = e_i X_ij + Q X
+// with X itself held to 22 bits as hi + lo in the first term, and only O, Q
+// and hi are fp16 operands.  Measured against 64 bits over flat, decaying and
+// low-rank spectra: 2^-10 of the result's norm or less.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "linear_common.h"
+#include "linear_plan.h"
+#include "linear_tiles.h"
+#include "zero_muon.h"
+
+namespace {
+
+using namespace zero_host;
+using namespace zero_linear_impl;
+
+constexpr float kScale = 4096.0f, kInv = 1.0f / 4096.0f, kInv2 = kInv * kInv;
+constexpr int kParts = 256;  // partial sums of squares a matrix
+constexpr int64_t kMaxSide = 65536, kMaxCount = 65535;
+
+struct Input {
+    const void *u;
+    int64_t ldu, su;
+    int32_t rows, cols;  // as the caller has it
+};
+
+// element (i, j) of the caller's matrix
+template <int DT>
+__device__ __forceinline__ float element(const void *p, int64_t at) {
+    if constexpr (DT == ZERO_FP32) return static_cast<const float *>(p)[at];
+    const uint16_t h = static_cast<const uint16_t *>(p)[at];
+    return DT == ZERO_BF16 ? BF16::up(h) : FP16::up(h);
+}
+
+template <int DT>
+__device__ __forceinline__ void eight(const void *p, int64_t at, int n, float (&v)[8]) {
+    if (n >= 8) {
+        if constexpr (DT == ZERO_FP32) {
+            const float *q = static_cast<const float *>(p) + at;
+            const f32x4 a = load32(q, 4), b = load32(q + 4, 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = a[e];
+                v[4 + e] = b[e];
+            }
+        } else {
+            f32x4 a, b;
+            const uint16_t *q = static_cast<const uint16_t *>(p) + at;
+            if (DT == ZERO_BF16)
+                load16x8<BF16>(q, a, b);
+            else
+                load16x8<FP16>(q, a, b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = a[e];
+                v[4 + e] = b[e];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < n ? element<DT>(p, at + e) : 0.0f;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// |U|^2 in kParts fp64 parts a matrix: pieces of eight elements, in turn
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+    return v;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) squares_kernel(Input in, double *parts) {
+    __shared__ double wave_part[4];
+    const uint32_t a_row = static_cast<uint32_t>(in.cols + 7) / 8;
+    const uint32_t total = a_row * static_cast<uint32_t>(in.rows);
+    const int64_t base = static_cast<int64_t>(blockIdx.y) * in.su;
+    double s = 0.0;
+    for (uint32_t p = blockIdx.x * 256u + threadIdx.x; p < total; p += kParts * 256u) {
+        const uint32_t i = p / a_row, j = (p - i * a_row) * 8u;
+        float v[8];
+        eight<DT>(in.u, base + i * in.ldu + j, in.cols - static_cast<int>(j), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const double d = static_cast<double>(v[e]);
+            s = __builtin_fma(d, d, s);
+        }
+    }
+    s = wave_sum(s);
+    if ((threadIdx.x & 63) == 0) wave_part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        parts[static_cast<int64_t>(blockIdx.y) * kParts + blockIdx.x] =
+            ((wave_part[0] + wave_part[1]) + wave_part[2]) + wave_part[3];
+}
+
+// ---------------------------------------------------------------------------
+// X = U / (|U| + eps) (or its transpose), scaled, as hi and lo; zeros in the
+// padding.  A workgroup has 64 x 64 of it.
+
+__device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
+    hi = FP16::down(v);
+    lo = FP16::down(v - FP16::up(hi));
+}
+
+template <int DT, bool TALL>
+__global__ void __launch_bounds__(256) spread_kernel(Input in, const double *parts, double eps,
+                                                     uint16_t *hi, uint16_t *lo, int32_t rp,
+                                                     int32_t cp) {
+    __shared__ double wave_part[4];
+    __shared__ float block[TALL ? 64 : 1][65];
+    const int t = threadIdx.x;
+    const int64_t m = blockIdx.z;
+    double s = wave_sum(parts[m * kParts + t]);
+    if ((t & 63) == 0) wave_part[t >> 6] = s;
+    __syncthreads();
+    s = ((wave_part[0] + wave_part[1]) + wave_part[2]) + wave_part[3];
+    const double norm = sqrt(s) + eps;
+    // an Inf or a NaN anywhere makes the matrix NaN
+    const double inv = norm - norm == 0.0 ? static_cast<double>(kScale) / norm : norm - norm;
+    const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
+    const int64_t base = m * in.su;
+    if (TALL) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int y = (t >> 3) + 32 * h, x = (t & 7) * 8;  // u row j0 + y, columns i0 + x..
+            float v[8];
+            eight<DT>(in.u, base + (j0 + y) * in.ldu + i0 + x,
+                      j0 + y < in.rows ? in.cols - (i0 + x) : 0, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) block[y][x + e] = v[e];
+        }
+        __syncthreads();
+    }
+    const int r = TALL ? in.cols : in.rows, c = TALL ? in.rows : in.cols;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int y = (t >> 3) + 32 * h, x = (t & 7) * 8, i = i0 + y, j = j0 + x;
+        float v[8];
+        if (TALL) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = block[x + e][y];
+        } else {
+            eight<DT>(in.u, base + i * in.ldu + j, i < r ? c - j : 0, v);
+        }
+        u16x8 a, b;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint16_t p = 0, q = 0;
+            if (i < r && j + e < c)
+                split(static_cast<float>(static_cast<double>(v[e]) * inv), p, q);
+            a[e] = p;
+            b[e] = q;
+        }
+        const int64_t at = (m * rp + i) * cp + j;
+        *reinterpret_cast<u16x8 *>(hi + at) = a;
+        *reinterpret_cast<u16x8 *>(lo + at) = b;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the products
+
+enum Kind { GRAM = 0, SQUARE = 1, APPLY = 2, FINISH = 3 };  // FINISH: the last apply
+
+struct Args {
+    const uint16_t *p, *q;      // the product's operands
+    const uint16_t *hi, *lo;    // square: O in hi; apply: X
+    uint16_t *out, *out_lo;     // the fp16 result; apply: the new X
+    const float *diag;          // square: d of A; apply: e of P
+    float *new_diag;            // gram: d; square: e
+    void *o;                    // finish: the caller's result
+    int64_t ldo, so;
+    int32_t r, c;               // of X, without padding
+    int32_t rp, cp;
+    int32_t tiles, tiles_j, count;
+    float ca, cb, cc;
+    int32_t tall, bf16;
+};
+
+// Which tile of which matrix a workgroup has.  Workgroups go round the 8 XCDs
+// in turn; each XCD is given one contiguous run of tiles.
+__device__ __forceinline__ int run_of(int b, int total) {
+    const int x = b & 7, q = total >> 3, r = total & 7;
+    return x * q + (x < r ? x : r) + (b >> 3);
+}
+
+template <int KIND, int BT, int WI, int WJ>
+__global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
+    constexpr bool SYM = KIND == GRAM || KIND == SQUARE, QKC = SYM;
+    constexpr int THREADS = WI * WJ * kWave;
+    constexpr int FI = BT / WI / 16, FJ = BT / WJ / 16;
+    constexpr int SLOT = kTile<true, BT> + kTile<QKC, BT>;
+    __shared__ __attribute__((aligned(1024))) uint16_t tiles[2 * SLOT];
+
+    const int id = run_of(static_cast<int>(blockIdx.x), a.tiles * a.count);
+    const int m = __builtin_amdgcn_readfirstlane(id / a.tiles), in = id - m * a.tiles;
+    int ti, tj;
+    if (SYM) {  // the lower triangle, row by row
+        ti = static_cast<int>((sqrtf(8.0f * static_cast<float>(in) + 1.0f) - 1.0f) * 0.5f);
+        while ((ti + 1) * (ti + 2) / 2 <= in) ++ti;
+        while (ti * (ti + 1) / 2 > in) --ti;
+        tj = in - ti * (ti + 1) / 2;
+    } else {
+        const int rows = a.tiles / a.tiles_j, band = 8 * a.tiles_j, first = in / band * 8;
+        const int high = min(8, rows - first), k = in - first * a.tiles_j;
+        ti = first + k % high;
+        tj = k / high;
+    }
+    ti = __builtin_amdgcn_readfirstlane(ti);
+    tj = __builtin_amdgcn_readfirstlane(tj);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int wi = wave / WJ * (BT / WI), wj = wave % WJ * (BT / WJ);
+    const int i0 = ti * BT, j0 = tj * BT;
+    const int nj = SYM ? a.rp : a.cp, nc = KIND == GRAM ? a.cp : a.rp;
+    const int64_t px = static_cast<int64_t>(m) * a.rp * a.cp;
+    const int64_t pa = static_cast<int64_t>(m) * a.rp * a.rp;
+    const int64_t pd = static_cast<int64_t>(m) * a.rp;
+
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int f = 0; f < FI; ++f)
+#pragma unroll
+        for (int t = 0; t < FJ; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    Direct<true, BT, THREADS, false> dp;
+    Direct<QKC, BT, THREADS, true> dq;
+    constexpr int NP = Direct<true, BT, THREADS, false>::N;
+    constexpr int NQ = Direct<QKC, BT, THREADS, true>::N;
+    dp.init(a.p + (KIND == GRAM ? px : pa), nc, i0, a.rp, 0);
+    dq.init(a.q + (KIND == SQUARE ? pa : px), SYM ? nc : nj, j0, nj, 0);
+    const uint32_t lds = static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t *)tiles));
+    auto slot_of = [&](int s) __attribute__((always_inline)) { return (s & 1) * SLOT; };
+    auto copy = [&](int n, int s) __attribute__((always_inline)) {
+        if (n < NP)
+            dp.issue(n, lds + 2 * slot_of(s), wave);
+        else if (n < NP + NQ)
+            dq.issue(n - NP, lds + 2 * (slot_of(s) + kTile<true, BT>), wave);
+    };
+    auto copied = [&]() __attribute__((always_inline)) {
+        dp.next();
+        dq.next();
+    };
+    s16x8 fp[2][FI], fq[2][FJ];
+    auto read = [&](int n, int s, int kk) __attribute__((always_inline)) {
+        const uint16_t *tp = tiles + slot_of(s), *tq = tp + kTile<true, BT>;
+        if (n < FJ)
+            fq[kk][n] = fragment<QKC, BT, true>(tq, wj, n, kk, lane);
+        else if (n < FJ + FI)
+            fp[kk][n - FJ] = fragment<true, BT, false>(tp, wi, n - FJ, kk, lane);
+    };
+    // The main loop of the layer products: steps of 64 of the contraction in
+    // two buffers, each in two halves of 32 whose products, reads of the other
+    // half and (second half) copies of the step after next are dealt out one
+    // by one; one barrier a step.
+    auto half = [&](auto kk_, auto copy_, int rs, int cs) __attribute__((always_inline)) {
+        constexpr int kk = decltype(kk_)::value, READS = FI + FJ, N = FI * FJ;
+        constexpr int M = N * 3 / 4 > 0 ? N * 3 / 4 : 1;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            bool placed = false;
+#pragma unroll
+            for (int r = 0; r < READS; ++r)
+                if (r * M / READS == n) {
+                    read(r, rs, 1 - kk);
+                    placed = true;
+                }
+            if (decltype(copy_)::value) {
+#pragma unroll
+                for (int c = 0; c < NP + NQ; ++c)
+                    if (c * M / (NP + NQ) == n) {
+                        copy(c, cs);
+                        placed = true;
+                    }
+            }
+            acc[n / FJ][n % FJ] =
+                mfma<FP16>(fq[kk][n % FJ], fp[kk][n / FJ], acc[n / FJ][n % FJ]);
+            if (placed) __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    using first_half = std::integral_constant<int, 0>;
+    using second_half = std::integral_constant<int, 1>;
+    auto arrive = [&]() __attribute__((always_inline)) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const int steps = nc / kBK;  // at least one
+#pragma unroll
+    for (int n = 0; n < NP + NQ; ++n) copy(n, 0);
+    copied();
+    arrive();
+    if (steps > 1) {
+#pragma unroll
+        for (int n = 0; n < NP + NQ; ++n) copy(n, 1);
+        copied();
+    }
+#pragma unroll
+    for (int n = 0; n < FI + FJ; ++n) read(n, 0, 0);
+    int s = 0;
+#pragma unroll 1
+    for (; s < steps - 2; ++s) {
+        half(first_half{}, std::false_type{}, s, 0);
+        arrive();
+        half(second_half{}, std::true_type{}, s + 1, s + 2);
+        copied();
+    }
+#pragma unroll 1
+    for (; s < steps; ++s) {
+        half(first_half{}, std::false_type{}, s, 0);
+        arrive();
+        half(second_half{}, std::false_type{}, s + 1, 0);
+    }
+
+    // eight neighbouring results (i, j..j+7) a lane
+    const int g = lane >> 4;
+#pragma unroll
+    for (int f = 0; f < FI; ++f) {
+        const int i = i0 + wi + f * 16 + (lane & 15);
+#pragma unroll
+        for (int p = 0; p < FJ / 2; ++p) {
+            const int j = j0 + wj + p * 32 + g * 8;
+            if (i >= a.rp || j >= nj) continue;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = acc[f][2 * p][e];
+                v[4 + e] = acc[f][2 * p + 1][e];
+            }
+            if constexpr (KIND == GRAM) {
+                u16x8 h;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (i == j + e) a.new_diag[pd + i] = v[e] * kInv2;
+                    h[e] = i == j + e ? 0 : FP16::down(v[e] * kInv);
+                }
+                uint16_t *o = a.out + pa;
+                *reinterpret_cast<u16x8 *>(o + static_cast<int64_t>(i) * a.rp + j) = h;
+                if (ti != tj) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[static_cast<int64_t>(j + e) * a.rp + i] = h[e];
+                }
+            } else if constexpr (KIND == SQUARE) {
+                const u16x8 oh = *reinterpret_cast<const u16x8 *>(
+                    a.hi + pa + static_cast<int64_t>(i) * a.rp + j);
+                const float di = a.diag[pd + i];
+                f32x4 dj[2];
+                dj[0] = *reinterpret_cast<const f32x4 *>(a.diag + pd + j);
+                dj[1] = *reinterpret_cast<const f32x4 *>(a.diag + pd + j + 4);
+                u16x8 h;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float oo = v[e] * kInv2, oij = FP16::up(oh[e]) * kInv;
+                    if (i == j + e)
+                        a.new_diag[pd + i] = a.ca + a.cb * di + a.cc * (oo + di * di);
+                    const float sq = __builtin_fmaf(di + dj[e >> 2][e & 3], oij, oo);
+                    const float q = __builtin_fmaf(a.cc, sq, a.cb * oij) * kScale;
+                    h[e] = i == j + e ? 0 : FP16::down(q);
+                }
+                uint16_t *o = a.out + pa;
+                *reinterpret_cast<u16x8 *>(o + static_cast<int64_t>(i) * a.rp + j) = h;
+                if (ti != tj) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[static_cast<int64_t>(j + e) * a.rp + i] = h[e];
+                }
+            } else {
+                const int64_t at = px + static_cast<int64_t>(i) * a.cp + j;
+                const u16x8 xh = *reinterpret_cast<const u16x8 *>(a.hi + at);
+                const u16x8 xl = *reinterpret_cast<const u16x8 *>(a.lo + at);
+                const float ei = a.diag[pd + i];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = __builtin_fmaf(ei, FP16::up(xh[e]) + FP16::up(xl[e]), v[e] * kInv);
+                if constexpr (KIND == APPLY) {
+                    u16x8 nh, nl;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint16_t x, y;
+                        split(v[e], x, y);
+                        nh[e] = x;
+                        nl[e] = y;
+                    }
+                    *reinterpret_cast<u16x8 *>(a.out + at) = nh;
+                    *reinterpret_cast<u16x8 *>(a.out_lo + at) = nl;
+                } else if (i < a.r) {
+                    uint16_t *o = static_cast<uint16_t *>(a.o) + m * a.so;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint16_t h =
+                            a.bf16 ? BF16::down(v[e] * kInv) : FP16::down(v[e] * kInv);
+                        if (j + e < a.c)
+                            o[a.tall ? (j + e) * a.ldo + i : i * a.ldo + j + e] = h;
+                    }
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+inline int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
+
+struct Work {
+    int64_t r, c, rp, cp;
+    int64_t parts, d, e, a, q, hi0, hi1, lo, bytes;  // offsets into the workspace
+};
+
+Work work_of(int64_t count, int64_t rows, int64_t cols) {
+    Work w{};
+    w.r = std::min(rows, cols);
+    w.c = std::max(rows, cols);
+    w.rp = up64(w.r);
+    w.cp = up64(w.c);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    w.parts = take(count * kParts * 8);
+    w.d = take(count * w.rp * 4);
+    w.e = take(count * w.rp * 4);
+    w.a = take(count * w.rp * w.rp * 2);
+    w.q = take(count * w.rp * w.rp * 2);
+    w.hi0 = take(count * w.rp * w.cp * 2);
+    w.hi1 = take(count * w.rp * w.cp * 2);
+    w.lo = take(count * w.rp * w.cp * 2);
+    w.bytes = at;
+    return w;
+}
+
+bool sides_ok(int64_t count, int64_t rows, int64_t cols) {
+    return count >= 0 && count <= kMaxCount && rows >= 0 && rows <= kMaxSide && cols >= 0 &&
+           cols <= kMaxSide;
+}
+
+constexpr int64_t kMaxTiles = int64_t(1) << 23;
+
+int64_t tiles_of(int kind, const Work &w, int64_t bt) {
+    const int64_t ti = ceil_div(w.rp, bt);
+    return kind == GRAM || kind == SQUARE ? ti * (ti + 1) / 2 : ti * ceil_div(w.cp, bt);
+}
+
+// the side of a product's tiles
+int tile_side(int kind, const Work &w, int64_t count) {
+    if (count * tiles_of(kind, w, 256) >= 128) return 256;
+    return count * tiles_of(kind, w, 128) >= 128 ? 128 : 64;
+}
+
+template <int KIND>
+zero_status run(Args a, const Work &w, hipStream_t st) {
+    const int bt = tile_side(KIND, w, a.count);
+    const int64_t tiles = tiles_of(KIND, w, bt), groups = tiles * a.count;
+    if (groups >= kMaxTiles) return ZERO_EINVAL;
+    a.tiles = static_cast<int32_t>(tiles);
+    a.tiles_j = static_cast<int32_t>(ceil_div(w.cp, bt));
+    const uint32_t n = static_cast<uint32_t>(groups);
+    if (bt == 256)
+        product_kernel<KIND, 256, 2, 4><<<n, 512, 0, st>>>(a);
+    else if (bt == 128)
+        product_kernel<KIND, 128, 2, 2><<<n, 256, 0, st>>>(a);
+    else
+        product_kernel<KIND, 64, 2, 2><<<n, 256, 0, st>>>(a);
+    return launch_status();
+}
+
+template <int DT>
+void spread(const Input &in, const Work &w, int64_t count, double eps, char *ws, bool tall,
+            hipStream_t st) {
+    auto *parts = reinterpret_cast<double *>(ws + w.parts);
+    auto *hi = reinterpret_cast<uint16_t *>(ws + w.hi0);
+    auto *lo = reinterpret_cast<uint16_t *>(ws + w.lo);
+    const uint32_t n = static_cast<uint32_t>(count);
+    squares_kernel<DT><<<dim3(kParts, n), 256, 0, st>>>(in, parts);
+    const dim3 grid(static_cast<uint32_t>(w.cp / 64), static_cast<uint32_t>(w.rp / 64), n);
+    const int32_t rp = static_cast<int32_t>(w.rp), cp = static_cast<int32_t>(w.cp);
+    if (tall)
+        spread_kernel<DT, true><<<grid, 256, 0, st>>>(in, parts, eps, hi, lo, rp, cp);
+    else
+        spread_kernel<DT, false><<<grid, 256, 0, st>>>(in, parts, eps, hi, lo, rp, cp);
+}
+
+// a stack of count matrices: the span of all, and whether its strides hold
+bool stack_ok(const Mat &one, int64_t count, int64_t stride, Span *all) {
+    if (!one.ok()) return false;
+    if (count > 1 && (stride < one.extent() || stride > (kMaxSpan - one.extent()) / (count - 1)))
+        return false;
+    *all = span_of(one.p, (count - 1) * (count > 1 ? stride : 0) + one.extent(), one.elem);
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t zero_orthogonalize_workspace_bytes(int64_t count, int64_t rows, int64_t cols) {
+    if (!sides_ok(count, rows, cols)) return -1;
+    if (count == 0 || rows == 0 || cols == 0) return 0;
+    return work_of(count, rows, cols).bytes;
+}
+
+zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64_t su,
+                               int64_t count, int64_t rows, int64_t cols,
+                               const zero_ns_params *ns, void *o, zero_dtype odt, int64_t ldo,
+                               int64_t so, void *workspace, int64_t workspace_bytes,
+                               void *stream) {
+    const zero_ns_params usual{5, 0, 1e-7, nullptr};
+    const zero_ns_params &k = ns != nullptr ? *ns : usual;
+    if ((!is16(udt) && udt != ZERO_FP32) || !is16(odt) || !sides_ok(count, rows, cols))
+        return ZERO_EINVAL;
+    if (k.steps < 1 || k.steps > ZERO_NS_MAX_STEPS || !(std::isfinite(k.eps) && k.eps >= 0.0))
+        return ZERO_EINVAL;
+    for (int i = 0; k.coeffs != nullptr && i < 3 * k.steps; ++i)
+        if (!std::isfinite(k.coeffs[i])) return ZERO_EINVAL;
+    if (count == 0 || rows == 0 || cols == 0) return ZERO_OK;
+    Span si, sr;
+    if (!stack_ok(Mat{u, rows, cols, ldu, size_of(udt)}, count, su, &si) ||
+        !stack_ok(Mat{o, rows, cols, ldo, 2}, count, so, &sr))
+        return ZERO_EINVAL;
+    const Work w = work_of(count, rows, cols);
+    if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < w.bytes)
+        return ZERO_EINVAL;
+    const Span sw = span_of(workspace, w.bytes, 1);
+    if (overlap(sr, si) || overlap(sr, sw) || overlap(si, sw)) return ZERO_EALIAS;
+
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    const bool tall = rows > cols;
+    const Input in{u, ldu, su, static_cast<int32_t>(rows), static_cast<int32_t>(cols)};
+    if (udt == ZERO_BF16)
+        spread<ZERO_BF16>(in, w, count, k.eps, ws, tall, st);
+    else if (udt == ZERO_FP16)
+        spread<ZERO_FP16>(in, w, count, k.eps, ws, tall, st);
+    else
+        spread<ZERO_FP32>(in, w, count, k.eps, ws, tall, st);
+
+    uint16_t *hi[2] = {reinterpret_cast<uint16_t *>(ws + w.hi0),
+                       reinterpret_cast<uint16_t *>(ws + w.hi1)};
+    uint16_t *lo = reinterpret_cast<uint16_t *>(ws + w.lo);
+    uint16_t *A = reinterpret_cast<uint16_t *>(ws + w.a);
+    uint16_t *Q = reinterpret_cast<uint16_t *>(ws + w.q);
+    float *d = reinterpret_cast<float *>(ws + w.d), *e = reinterpret_cast<float *>(ws + w.e);
+    Args base{};
+    base.r = static_cast<int32_t>(w.r);
+    base.c = static_cast<int32_t>(w.c);
+    base.rp = static_cast<int32_t>(w.rp);
+    base.cp = static_cast<int32_t>(w.cp);
+    base.count = static_cast<int32_t>(count);
+    base.o = o;
+    base.ldo = ldo;
+    base.so = so;
+    base.tall = tall;
+    base.bf16 = odt == ZERO_BF16;
+    zero_status status = launch_status();
+    for (int i = 0; i < k.steps && status == ZERO_OK; ++i) {
+        const double usual_coeffs[3] = {3.4445, -4.7750, 2.0315};
+        const double *c = k.coeffs != nullptr ? k.coeffs + 3 * i : usual_coeffs;
+        const uint16_t *x = hi[i & 1];
+        Args g = base;
+        g.p = g.q = x;
+        g.out = A;
+        g.new_diag = d;
+        status = run<GRAM>(g, w, st);
+        if (status != ZERO_OK) break;
+        Args s = base;
+        s.p = s.q = s.hi = A;
+        s.out = Q;
+        s.diag = d;
+        s.new_diag = e;
+        s.ca = static_cast<float>(c[0]);
+        s.cb = static_cast<float>(c[1]);
+        s.cc = static_cast<float>(c[2]);
+        status = run<SQUARE>(s, w, st);
+        if (status != ZERO_OK) break;
+        Args p = base;
+        p.p = Q;
+        p.q = p.hi = x;
+        p.lo = lo;
+        p.out = hi[(i + 1) & 1];
+        p.out_lo = lo;
+        p.diag = e;
+        status = i + 1 < k.steps ? run<APPLY>(p, w, st) : run<FINISH>(p, w, st);
+    }
+    return status;
+}
+
+}  // extern "C"
