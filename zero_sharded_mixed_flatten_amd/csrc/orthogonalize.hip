@@ -209,6 +209,15 @@ __device__ __forceinline__ int run_of(int b, int total) {
     return x * q + (x < r ? x : r) + (b >> 3);
 }
 
+// the address in scalar registers, which the direct copies need it in
+template <class P>
+__device__ __forceinline__ P *uniform(P *p) {
+    const uint64_t v = reinterpret_cast<uintptr_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32));
+    return reinterpret_cast<P *>(static_cast<uintptr_t>(static_cast<uint64_t>(hi) << 32 | lo));
+}
+
 template <int KIND, int BT, int WI, int WJ>
 __global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
     constexpr bool SYM = KIND == GRAM || KIND == SQUARE, QKC = SYM;
@@ -253,6 +262,8 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
     constexpr int NQ = Direct<QKC, BT, THREADS, true>::N;
     dp.init(a.p + (KIND == GRAM ? px : pa), nc, i0, a.rp, 0);
     dq.init(a.q + (KIND == SQUARE ? pa : px), SYM ? nc : nj, j0, nj, 0);
+    dp.base = uniform(dp.base);
+    dq.base = uniform(dq.base);
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t *)tiles));
     auto slot_of = [&](int s) __attribute__((always_inline)) { return (s & 1) * SLOT; };
@@ -339,87 +350,132 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
         half(second_half{}, std::false_type{}, s + 1, 0);
     }
 
-    // eight neighbouring results (i, j..j+7) a lane
+    // Eight neighbouring results (i, j..j+7) a lane and unit.  The loads of X
+    // (or O) run a group of units ahead of the stores, since a load behind a
+    // store waits for it: four 4096 x 4096 matrices 505 us; one unit after the
+    // other 538, all loads before all stores 541.
     const int g = lane >> 4;
+    constexpr int UNITS = FI * FJ / 2, GROUP = UNITS < 4 ? UNITS : 4, GROUPS = UNITS / GROUP;
+    // places in the tile, whose own place is in scalar registers
+    const int in_i = wi + (lane & 15), in_j = wj + g * 8;
+    const int rows = a.rp - i0, columns = nj - j0, ld = SYM ? a.rp : a.cp;
+    const int64_t corner = (SYM ? pa : px) + static_cast<int64_t>(i0) * ld + j0;
+    auto row_of = [&](int u) __attribute__((always_inline)) { return in_i + u / (FJ / 2) * 16; };
+    auto column_of = [&](int u) __attribute__((always_inline)) {
+        return in_j + u % (FJ / 2) * 32;
+    };
+    auto offset = [&](int i, int j) __attribute__((always_inline)) {
+        return static_cast<uint32_t>(i * ld + j);
+    };
+    uint16_t *tile = KIND == FINISH ? nullptr : uniform(a.out + corner);
+    uint16_t *tile_lo = KIND == APPLY ? uniform(a.out_lo + corner) : nullptr;
+    auto store = [&](int u) __attribute__((always_inline)) {
+        const int i = row_of(u), j = column_of(u), f = u / (FJ / 2), p = u % (FJ / 2);
+        if (i >= rows || j >= columns) return;
+        float v[8];
 #pragma unroll
-    for (int f = 0; f < FI; ++f) {
-        const int i = i0 + wi + f * 16 + (lane & 15);
+        for (int e = 0; e < 8; ++e) v[e] = acc[f][2 * p + e / 4][e & 3];
+        if constexpr (SYM) {
+            // the diagonal in fp32 (gram: d; square: e), zero in the fp16 matrix
+            u16x8 h;
 #pragma unroll
-        for (int p = 0; p < FJ / 2; ++p) {
-            const int j = j0 + wj + p * 32 + g * 8;
-            if (i >= a.rp || j >= nj) continue;
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = acc[f][2 * p][e];
-                v[4 + e] = acc[f][2 * p + 1][e];
+            for (int e = 0; e < 8; ++e) {
+                const bool diagonal = ti == tj && i == j + e;
+                if (diagonal) a.new_diag[pd + i0 + i] = KIND == GRAM ? v[e] * kInv2 : v[e];
+                h[e] = diagonal ? 0 : FP16::down(KIND == GRAM ? v[e] * kInv : v[e]);
             }
-            if constexpr (KIND == GRAM) {
-                u16x8 h;
+            *reinterpret_cast<u16x8 *>(tile + offset(i, j)) = h;
+            if (ti != tj) {
+                uint16_t *o = a.out + pa + static_cast<int64_t>(j0 + j) * a.rp + i0 + i;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (i == j + e) a.new_diag[pd + i] = v[e] * kInv2;
-                    h[e] = i == j + e ? 0 : FP16::down(v[e] * kInv);
-                }
-                uint16_t *o = a.out + pa;
-                *reinterpret_cast<u16x8 *>(o + static_cast<int64_t>(i) * a.rp + j) = h;
-                if (ti != tj) {
+                for (int e = 0; e < 8; ++e) o[e * a.rp] = h[e];
+            }
+        } else if constexpr (KIND == APPLY) {
+            u16x8 nh, nl;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[static_cast<int64_t>(j + e) * a.rp + i] = h[e];
-                }
-            } else if constexpr (KIND == SQUARE) {
-                const u16x8 oh = *reinterpret_cast<const u16x8 *>(
-                    a.hi + pa + static_cast<int64_t>(i) * a.rp + j);
-                const float di = a.diag[pd + i];
-                f32x4 dj[2];
-                dj[0] = *reinterpret_cast<const f32x4 *>(a.diag + pd + j);
-                dj[1] = *reinterpret_cast<const f32x4 *>(a.diag + pd + j + 4);
-                u16x8 h;
+            for (int e = 0; e < 8; ++e) {
+                uint16_t x, y;
+                split(v[e], x, y);
+                nh[e] = x;
+                nl[e] = y;
+            }
+            *reinterpret_cast<u16x8 *>(tile + offset(i, j)) = nh;
+            *reinterpret_cast<u16x8 *>(tile_lo + offset(i, j)) = nl;
+        } else if (i0 + i < a.r) {
+            uint16_t *o = static_cast<uint16_t *>(a.o) + m * a.so;
+            const int64_t gi = i0 + i, gj = j0 + j;
+            u16x8 h;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float oo = v[e] * kInv2, oij = FP16::up(oh[e]) * kInv;
-                    if (i == j + e)
-                        a.new_diag[pd + i] = a.ca + a.cb * di + a.cc * (oo + di * di);
-                    const float sq = __builtin_fmaf(di + dj[e >> 2][e & 3], oij, oo);
-                    const float q = __builtin_fmaf(a.cc, sq, a.cb * oij) * kScale;
-                    h[e] = i == j + e ? 0 : FP16::down(q);
-                }
-                uint16_t *o = a.out + pa;
-                *reinterpret_cast<u16x8 *>(o + static_cast<int64_t>(i) * a.rp + j) = h;
-                if (ti != tj) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[static_cast<int64_t>(j + e) * a.rp + i] = h[e];
-                }
+            for (int e = 0; e < 8; ++e)
+                h[e] = a.bf16 ? BF16::down(v[e] * kInv) : FP16::down(v[e] * kInv);
+            if (!a.tall && gj + 8 <= a.c) {
+                __builtin_memcpy(o + gi * a.ldo + gj, &h, 16);
             } else {
-                const int64_t at = px + static_cast<int64_t>(i) * a.cp + j;
-                const u16x8 xh = *reinterpret_cast<const u16x8 *>(a.hi + at);
-                const u16x8 xl = *reinterpret_cast<const u16x8 *>(a.lo + at);
-                const float ei = a.diag[pd + i];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] = __builtin_fmaf(ei, FP16::up(xh[e]) + FP16::up(xl[e]), v[e] * kInv);
-                if constexpr (KIND == APPLY) {
-                    u16x8 nh, nl;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint16_t x, y;
-                        split(v[e], x, y);
-                        nh[e] = x;
-                        nl[e] = y;
-                    }
-                    *reinterpret_cast<u16x8 *>(a.out + at) = nh;
-                    *reinterpret_cast<u16x8 *>(a.out_lo + at) = nl;
-                } else if (i < a.r) {
-                    uint16_t *o = static_cast<uint16_t *>(a.o) + m * a.so;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint16_t h =
-                            a.bf16 ? BF16::down(v[e] * kInv) : FP16::down(v[e] * kInv);
-                        if (j + e < a.c)
-                            o[a.tall ? (j + e) * a.ldo + i : i * a.ldo + j + e] = h;
-                    }
-                }
+                    if (gj + e < a.c)
+                        o[a.tall ? (gj + e) * a.ldo + gi : gi * a.ldo + gj + e] = h[e];
             }
+        }
+    };
+    if constexpr (KIND == GRAM) {
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) store(u);
+    }
+    if constexpr (KIND != GRAM) {
+        u16x8 xh[2][GROUP], xl[2][KIND == SQUARE ? 1 : GROUP];
+        float ei[2][GROUP];
+        f32x4 dj[FJ];  // square: d of this lane's columns
+        if (KIND == SQUARE) {
+#pragma unroll
+            for (int t = 0; t < FJ; ++t) {
+                const int j = min(column_of(t / 2), columns - 8) + (t & 1) * 4;
+                dj[t] = *reinterpret_cast<const f32x4 *>(a.diag + pd + j0 + j);
+            }
+        }
+        const uint16_t *hi_tile = uniform(a.hi + corner);
+        const uint16_t *lo_tile = KIND == SQUARE ? nullptr : uniform(a.lo + corner);
+        const float *diag_tile = uniform(a.diag + pd + i0);
+        auto fetch = [&](int group) __attribute__((always_inline)) {
+#pragma unroll
+            for (int k = 0; k < GROUP; ++k) {
+                const int u = group * GROUP + k;
+                const uint32_t i = min(row_of(u), rows - 1);
+                const uint32_t at = offset(i, min(column_of(u), columns - 8));
+                xh[group & 1][k] = *reinterpret_cast<const u16x8 *>(hi_tile + at);
+                if (KIND != SQUARE)
+                    xl[group & 1][k] = *reinterpret_cast<const u16x8 *>(lo_tile + at);
+                ei[group & 1][k] = diag_tile[i];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        fetch(0);
+#pragma unroll
+        for (int group = 0; group < GROUPS; ++group) {
+            if (group + 1 < GROUPS) fetch(group + 1);
+#pragma unroll
+            for (int k = 0; k < GROUP; ++k) {
+                const int u = group * GROUP + k, f = u / (FJ / 2), p = u % (FJ / 2);
+                const u16x8 hi = xh[group & 1][k];
+                const float ri = ei[group & 1][k];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float v = acc[f][2 * p + e / 4][e & 3];
+                    if constexpr (KIND == SQUARE) {
+                        const float oo = v * kInv2, oij = FP16::up(hi[e]) * kInv;
+                        const float sq = __builtin_fmaf(ri + dj[2 * p + e / 4][e & 3], oij, oo);
+                        const bool diagonal = ti == tj && row_of(u) == column_of(u) + e;
+                        v = diagonal ? a.ca + a.cb * ri + a.cc * (oo + ri * ri)
+                                     : __builtin_fmaf(a.cc, sq, a.cb * oij) * kScale;
+                    } else {
+                        const u16x8 lo = xl[group & 1][k];
+                        v = __builtin_fmaf(ri, FP16::up(hi[e]) + FP16::up(lo[e]), v * kInv);
+                    }
+                    acc[f][2 * p + e / 4][e & 3] = v;
+                }
+                store(u);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
