@@ -324,3 +324,14 @@ def test_the_binding_refuses_what_does_not_fit():
         with pytest.raises((TypeError, ValueError)):
             zs.zero_muon_momentum(**{**dict(grads=w, n_rows=1, ld=100, length=100, mom=m,
                                             u=w.clone(), hp=hp), **bad})
+
+
+@pytest.mark.parametrize("count,r,c", [(4, 2300, 2500), (5, 2304, 2304), (1, 2900, 5200),
+                                       (2, 200, 9000), (1, 64, 7000), (1, 9000, 64)])
+def test_orthogonalize_large(count, r, c):
+    """tiles of 256 and their quarters, contractions in parts"""
+    u = torch.randn(count, r, c, generator=gen(r), device="cuda").to(BF)
+    o = torch.empty_like(u)
+    zs.zero_orthogonalize(u, o)
+    for i in range(count):
+        check_orth(o[i], ns64(u[i]), f"matrix {i}")

@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) tile_kernel(Args a) {
     Direct<QKC, BJ, THREADS, true> dq;
     constexpr int NP = Direct<PKC, BI, THREADS, false>::N, NQ = Direct<QKC, BJ, THREADS, true>::N;
     if (DIRECT) {
-        dp.init(a.p, a.ldp, i0, a.ni, c0);
-        dq.init(a.q, a.ldq, j0, a.nj, c0);
+        dp.init(a.p, a.ldp, i0, a.ni, c0, static_cast<int>(threadIdx.x));
+        dq.init(a.q, a.ldq, j0, a.nj, c0, static_cast<int>(threadIdx.x));
     }
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t *)tiles));

@@ -155,15 +155,16 @@ struct Direct {
     int64_t stride;         // bytes from step to step
     int64_t apart;          // bytes from copy to copy (rows of lanes)
     uint32_t off[KC ? N : 1];
+    // thread: of the THREADS that copy the tile
     __device__ __forceinline__ void init(const uint16_t *p, int64_t ld, int64_t r0, int64_t rows,
-                                         int64_t c0) {
+                                         int64_t c0, int thread) {
         base = reinterpret_cast<const char *>(KC ? p + r0 * ld + c0 : p + c0 * ld + r0);
         stride = (KC ? kBK : kBK * ld) * 2;
         apart = KC ? 0 : kRows * ld * 2;
         const int last = static_cast<int>(min(rows - r0, static_cast<int64_t>(ROWS))) - (KC ? 1 : 8);
 #pragma unroll
         for (int n = 0; n < (KC ? N : 1); ++n) {
-            const int pos = n * THREADS + static_cast<int>(threadIdx.x);
+            const int pos = n * THREADS + thread;
             const int row = piece_row<KC, ROWS>(pos), s = piece_slot<KC, ROWS, Q>(pos);
             off[n] = KC ? static_cast<uint32_t>(min(row, last)) * static_cast<uint32_t>(ld * 2) + s * 16
                         : static_cast<uint32_t>(row) * static_cast<uint32_t>(ld * 2) +

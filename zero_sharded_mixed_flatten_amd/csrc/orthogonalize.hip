@@ -197,7 +197,11 @@ struct Args {
     int64_t ldo, so;
     int32_t r, c;               // of X, without padding
     int32_t rp, cp;
-    int32_t tiles, tiles_j, count;
+    int32_t tiles, tiles_i, tiles_j, count;
+    int32_t parts, part_steps;  // gram
+    int32_t whole;   // tiles of 256 that the launch has, or
+    int32_t quarter; // >= 0: the workgroups are quarters of those from here on
+    f32x4 *partial;
     float ca, cb, cc;
     int32_t tall, bf16;
 };
@@ -218,15 +222,23 @@ __device__ __forceinline__ P *uniform(P *p) {
     return reinterpret_cast<P *>(static_cast<uintptr_t>(static_cast<uint64_t>(hi) << 32 | lo));
 }
 
-template <int KIND, int BT, int WI, int WJ>
-__global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
+// KG > 1: that many groups of waves share a workgroup and its tile, each with
+// buffers of its own and every KG-th step of the contraction, for products of
+// few tiles; their sums are added in their order at the end.
+// A gram product of few tiles and a long contraction is divided into a.parts
+// of it (blockIdx.y), whose fp32 sums lie in the workspace as the lanes hold
+// them; JOIN, a second launch, adds them in their order.
+template <int KIND, int BT, int WI, int WJ, int KG, bool JOIN = false>
+__global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kernel(Args a) {
     constexpr bool SYM = KIND == GRAM || KIND == SQUARE, QKC = SYM;
     constexpr int THREADS = WI * WJ * kWave;
     constexpr int FI = BT / WI / 16, FJ = BT / WJ / 16;
     constexpr int SLOT = kTile<true, BT> + kTile<QKC, BT>;
-    __shared__ __attribute__((aligned(1024))) uint16_t tiles[2 * SLOT];
+    __shared__ __attribute__((aligned(1024))) uint16_t all_tiles[KG * 2 * SLOT];
 
-    const int id = run_of(static_cast<int>(blockIdx.x), a.tiles * a.count);
+    const bool quarters = BT == 128 && a.quarter >= 0;
+    const int id = quarters ? a.quarter + static_cast<int>(blockIdx.x >> 2)
+                            : run_of(static_cast<int>(blockIdx.x), a.whole);
     const int m = __builtin_amdgcn_readfirstlane(id / a.tiles), in = id - m * a.tiles;
     int ti, tj;
     if (SYM) {  // the lower triangle, row by row
@@ -235,16 +247,23 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
         while (ti * (ti + 1) / 2 > in) --ti;
         tj = in - ti * (ti + 1) / 2;
     } else {
-        const int rows = a.tiles / a.tiles_j, band = 8 * a.tiles_j, first = in / band * 8;
-        const int high = min(8, rows - first), k = in - first * a.tiles_j;
+        const int band = 8 * a.tiles_j, first = in / band * 8;
+        const int high = min(8, a.tiles_i - first), k = in - first * a.tiles_j;
         ti = first + k % high;
         tj = k / high;
+    }
+    if (quarters) {
+        ti = 2 * ti + (blockIdx.x >> 1 & 1);
+        tj = 2 * tj + (blockIdx.x & 1);
+        if (ti * BT >= a.rp || tj * BT >= (SYM ? a.rp : a.cp) || (SYM && tj > ti)) return;
     }
     ti = __builtin_amdgcn_readfirstlane(ti);
     tj = __builtin_amdgcn_readfirstlane(tj);
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int any_wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int kg = any_wave / (WI * WJ), wave = any_wave % (WI * WJ);
     const int wi = wave / WJ * (BT / WI), wj = wave % WJ * (BT / WJ);
+    uint16_t *tiles = all_tiles + kg * 2 * SLOT;
     const int i0 = ti * BT, j0 = tj * BT;
     const int nj = SYM ? a.rp : a.cp, nc = KIND == GRAM ? a.cp : a.rp;
     const int64_t px = static_cast<int64_t>(m) * a.rp * a.cp;
@@ -256,14 +275,31 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
     for (int f = 0; f < FI; ++f)
 #pragma unroll
         for (int t = 0; t < FJ; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int g = lane >> 4;
+    auto sum_at = [&](int part, int f, int t) __attribute__((always_inline)) {
+        const int64_t tile = (static_cast<int64_t>(part) * a.count + m) * a.tiles + in;
+        return a.partial + tile * (BT * BT / 4) + ((f * FJ + t) * WI * WJ + wave) * kWave + lane;
+    };
+    if constexpr (JOIN) {
+        for (int part = 0; part < a.parts; ++part)
+#pragma unroll
+            for (int f = 0; f < FI; ++f)
+#pragma unroll
+                for (int t = 0; t < FJ; ++t) acc[f][t] += *sum_at(part, f, t);
+    } else {
+    const int c0 = KIND == GRAM ? static_cast<int>(blockIdx.y) * a.part_steps * kBK : 0;
     Direct<true, BT, THREADS, false> dp;
     Direct<QKC, BT, THREADS, true> dq;
     constexpr int NP = Direct<true, BT, THREADS, false>::N;
     constexpr int NQ = Direct<QKC, BT, THREADS, true>::N;
-    dp.init(a.p + (KIND == GRAM ? px : pa), nc, i0, a.rp, 0);
-    dq.init(a.q + (KIND == SQUARE ? pa : px), SYM ? nc : nj, j0, nj, 0);
+    dp.init(a.p + (KIND == GRAM ? px : pa), nc, i0, a.rp, c0 + kg * kBK,
+            wave * kWave + lane);
+    dq.init(a.q + (KIND == SQUARE ? pa : px), SYM ? nc : nj, j0, nj,
+            c0 + kg * kBK, wave * kWave + lane);
     dp.base = uniform(dp.base);
     dq.base = uniform(dq.base);
+    dp.stride *= KG;
+    dq.stride *= KG;
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t *)tiles));
     auto slot_of = [&](int s) __attribute__((always_inline)) { return (s & 1) * SLOT; };
@@ -323,10 +359,16 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-    const int steps = nc / kBK;  // at least one
+    // this group's steps; the groups meet at every barrier, also those that
+    // have none left
+    const int total = KIND == GRAM ? min(a.part_steps, nc / kBK - c0 / kBK) : nc / kBK;
+    const int most = (total + KG - 1) / KG;
+    const int steps = KG == 1 ? total : (total - kg + KG - 1) / KG;
+    if (steps > 0) {
 #pragma unroll
-    for (int n = 0; n < NP + NQ; ++n) copy(n, 0);
-    copied();
+        for (int n = 0; n < NP + NQ; ++n) copy(n, 0);
+        copied();
+    }
     arrive();
     if (steps > 1) {
 #pragma unroll
@@ -349,12 +391,60 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
         arrive();
         half(second_half{}, std::false_type{}, s + 1, 0);
     }
+    if constexpr (KG > 1) {
+        if (steps < most) arrive();  // one step fewer, at most
+        // each group has a share of the units to finish: the others' sums of
+        // these come through the buffers, which nobody reads any more
+        static_assert(FI % KG == 0 && (KG - 1) * 4 * BT * BT <= KG * 4 * SLOT, "the sums fit");
+        f32x4 *sums = reinterpret_cast<f32x4 *>(all_tiles);
+        constexpr int EACH = FI / KG * FJ * WI * WJ * kWave;  // of one group's share
+        arrive();
+#pragma unroll
+        for (int f = 0; f < FI; ++f) {
+            const int to = f / (FI / KG);
+            if (to == kg) continue;
+            const int slot = to * (KG - 1) + (kg < to ? kg : kg - 1);
+#pragma unroll
+            for (int t = 0; t < FJ; ++t)
+                sums[slot * EACH + ((f % (FI / KG) * FJ + t) * WI * WJ + wave) * kWave + lane] =
+                    acc[f][t];
+        }
+        arrive();
+#pragma unroll
+        for (int f = 0; f < FI; ++f) {
+            if (f / (FI / KG) != kg) continue;
+#pragma unroll
+            for (int t = 0; t < FJ; ++t) {
+                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < KG; ++k) {
+                    const int slot = kg * (KG - 1) + (k < kg ? k : k - 1);
+                    const f32x4 w =
+                        k == kg ? acc[f][t]
+                                : sums[slot * EACH +
+                                       ((f % (FI / KG) * FJ + t) * WI * WJ + wave) * kWave + lane];
+                    v = k == 0 ? w : v + w;
+                }
+                acc[f][t] = v;
+            }
+        }
+    }
+
+    if (KIND == GRAM && a.parts > 1) {
+#pragma unroll
+        for (int f = 0; f < FI; ++f) {
+            if (KG > 1 && f / (FI / KG) != kg) continue;
+#pragma unroll
+            for (int t = 0; t < FJ; ++t) *sum_at(blockIdx.y, f, t) = acc[f][t];
+        }
+        return;
+    }
+    }
 
     // Eight neighbouring results (i, j..j+7) a lane and unit.  The loads of X
     // (or O) run a group of units ahead of the stores, since a load behind a
     // store waits for it: four 4096 x 4096 matrices 505 us; one unit after the
     // other 538, all loads before all stores 541.
-    const int g = lane >> 4;
     constexpr int UNITS = FI * FJ / 2, GROUP = UNITS < 4 ? UNITS : 4, GROUPS = UNITS / GROUP;
     // places in the tile, whose own place is in scalar registers
     const int in_i = wi + (lane & 15), in_j = wj + g * 8;
@@ -418,9 +508,13 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
             }
         }
     };
+    auto mine = [&](int u) __attribute__((always_inline)) {
+        return KG == 1 || u / (UNITS / KG) == kg;
+    };
     if constexpr (KIND == GRAM) {
 #pragma unroll
-        for (int u = 0; u < UNITS; ++u) store(u);
+        for (int u = 0; u < UNITS; ++u)
+            if (mine(u)) store(u);
     }
     if constexpr (KIND != GRAM) {
         u16x8 xh[2][GROUP], xl[2][KIND == SQUARE ? 1 : GROUP];
@@ -440,6 +534,7 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
 #pragma unroll
             for (int k = 0; k < GROUP; ++k) {
                 const int u = group * GROUP + k;
+                if (!mine(u)) continue;
                 const uint32_t i = min(row_of(u), rows - 1);
                 const uint32_t at = offset(i, min(column_of(u), columns - 8));
                 xh[group & 1][k] = *reinterpret_cast<const u16x8 *>(hi_tile + at);
@@ -456,6 +551,7 @@ __global__ void __launch_bounds__(WI *WJ *kWave, 2) product_kernel(Args a) {
 #pragma unroll
             for (int k = 0; k < GROUP; ++k) {
                 const int u = group * GROUP + k, f = u / (FJ / 2), p = u % (FJ / 2);
+                if (!mine(u)) continue;
                 const u16x8 hi = xh[group & 1][k];
                 const float ri = ei[group & 1][k];
 #pragma unroll
@@ -487,8 +583,10 @@ inline int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 
 struct Work {
     int64_t r, c, rp, cp;
-    int64_t parts, d, e, a, q, hi0, hi1, lo, bytes;  // offsets into the workspace
+    int64_t parts, d, e, a, q, hi0, hi1, lo, partial, bytes;  // offsets into the workspace
 };
+
+int64_t partial_bytes(const Work &w, int64_t count);
 
 Work work_of(int64_t count, int64_t rows, int64_t cols) {
     Work w{};
@@ -510,6 +608,7 @@ Work work_of(int64_t count, int64_t rows, int64_t cols) {
     w.hi0 = take(count * w.rp * w.cp * 2);
     w.hi1 = take(count * w.rp * w.cp * 2);
     w.lo = take(count * w.rp * w.cp * 2);
+    w.partial = take(partial_bytes(w, count));
     w.bytes = at;
     return w;
 }
@@ -526,26 +625,78 @@ int64_t tiles_of(int kind, const Work &w, int64_t bt) {
     return kind == GRAM || kind == SQUARE ? ti * (ti + 1) / 2 : ti * ceil_div(w.cp, bt);
 }
 
-// the side of a product's tiles
-int tile_side(int kind, const Work &w, int64_t count) {
-    if (count * tiles_of(kind, w, 256) >= 128) return 256;
-    return count * tiles_of(kind, w, 128) >= 128 ? 128 : 64;
+// How a product runs: the side of its tiles, groups of waves a workgroup, and
+// (gram) parts of the contraction.
+struct Way {
+    int side, groups, parts;
+    int64_t steps;  // of a part
+};
+
+Way plan_of(int kind, const Work &w, int64_t count) {
+    const int64_t steps = (kind == GRAM ? w.cp : w.rp) / kBK;
+    const int64_t n256 = count * tiles_of(kind, w, 256), n128 = count * tiles_of(kind, w, 128),
+                  n64 = count * tiles_of(kind, w, 64);
+    Way p{64, 1, 1, steps};
+    if (n256 >= 128)
+        p.side = 256;
+    else if (n64 <= 384)
+        p.groups = steps > 2 ? 2 : 1;
+    else if (steps > 8)
+        p = Way{128, n128 <= 256 ? 2 : 1, 1, steps};
+    if (kind == GRAM && p.side == 64) {
+        const int64_t parts = std::min({steps / 8, 384 / n64, int64_t(10)});
+        if (parts > 1 && steps - steps / parts > 26) p.steps = ceil_div(steps, parts);
+        p.parts = static_cast<int>(ceil_div(steps, p.steps));
+    }
+    return p;
+}
+
+int64_t partial_bytes(const Work &w, int64_t count) {
+    const Way p = plan_of(GRAM, w, count);
+    return p.parts == 1 ? 0 : p.parts * count * tiles_of(GRAM, w, p.side) * p.side * p.side * 4;
 }
 
 template <int KIND>
 zero_status run(Args a, const Work &w, hipStream_t st) {
-    const int bt = tile_side(KIND, w, a.count);
-    const int64_t tiles = tiles_of(KIND, w, bt), groups = tiles * a.count;
-    if (groups >= kMaxTiles) return ZERO_EINVAL;
+    const Way p = plan_of(KIND, w, a.count);
+    const int64_t tiles = tiles_of(KIND, w, p.side), groups = tiles * a.count;
     a.tiles = static_cast<int32_t>(tiles);
-    a.tiles_j = static_cast<int32_t>(ceil_div(w.cp, bt));
-    const uint32_t n = static_cast<uint32_t>(groups);
-    if (bt == 256)
-        product_kernel<KIND, 256, 2, 4><<<n, 512, 0, st>>>(a);
-    else if (bt == 128)
-        product_kernel<KIND, 128, 2, 2><<<n, 256, 0, st>>>(a);
+    a.tiles_i = static_cast<int32_t>(ceil_div(w.rp, p.side));
+    a.tiles_j = static_cast<int32_t>(ceil_div(w.cp, p.side));
+    a.parts = p.parts;
+    a.part_steps = static_cast<int32_t>(p.steps);
+    // One tile of 256 has a CU to itself.  What is left after the last whole
+    // round of them, up to half a round, runs as quarters in a second launch.
+    // A call with and without, us: four 4096 x 4096 matrices 5390 : 5700, one
+    // 8192 x 8192 9470 : 10130, twelve 1600 x 1600 1680 : 1790; not where a few
+    // short tiles are left: sixteen 1600 x 1600 2120 : 2060.
+    int64_t rest = p.side == 256 ? quartered(groups) : 0;
+    if (rest * (KIND == GRAM ? w.cp : w.rp) < 65536) rest = 0;
+    a.whole = static_cast<int32_t>(groups - rest);
+    a.quarter = -1;
+    const uint32_t n = static_cast<uint32_t>(groups - rest);
+    const dim3 grid(n, static_cast<uint32_t>(p.parts));
+    if (p.side == 256) {
+        product_kernel<KIND, 256, 2, 4, 1><<<grid, 512, 0, st>>>(a);
+        a.quarter = static_cast<int32_t>(groups - rest);
+        if (rest > 64)
+            product_kernel<KIND, 128, 2, 2, 1>
+                <<<static_cast<uint32_t>(4 * rest), 256, 0, st>>>(a);
+        else if (rest > 0)
+            product_kernel<KIND, 128, 2, 2, 2>
+                <<<static_cast<uint32_t>(4 * rest), 512, 0, st>>>(a);
+    }
+    else if (p.side == 128 && p.groups == 1)
+        product_kernel<KIND, 128, 2, 2, 1><<<grid, 256, 0, st>>>(a);
+    else if (p.side == 128)
+        product_kernel<KIND, 128, 2, 2, 2><<<grid, 512, 0, st>>>(a);
+    else if (p.groups == 1)
+        product_kernel<KIND, 64, 2, 2, 1><<<grid, 256, 0, st>>>(a);
     else
-        product_kernel<KIND, 64, 2, 2><<<n, 256, 0, st>>>(a);
+        product_kernel<KIND, 64, 2, 2, 2><<<grid, 512, 0, st>>>(a);
+    if constexpr (KIND == GRAM) {
+        if (p.parts > 1) product_kernel<GRAM, 64, 2, 2, 1, true><<<n, 256, 0, st>>>(a);
+    }
     return launch_status();
 }
 
@@ -603,6 +754,11 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
         !stack_ok(Mat{o, rows, cols, ldo, 2}, count, so, &sr))
         return ZERO_EINVAL;
     const Work w = work_of(count, rows, cols);
+    // a launch has less than 2^32 threads
+    for (int kind : {GRAM, SQUARE, APPLY}) {
+        const Way p = plan_of(kind, w, count);
+        if (count * tiles_of(kind, w, p.side) * p.parts >= kMaxTiles) return ZERO_EINVAL;
+    }
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < w.bytes)
         return ZERO_EINVAL;
     const Span sw = span_of(workspace, w.bytes, 1);
@@ -636,6 +792,7 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     base.so = so;
     base.tall = tall;
     base.bf16 = odt == ZERO_BF16;
+    base.partial = reinterpret_cast<f32x4 *>(ws + w.partial);
     zero_status status = launch_status();
     for (int i = 0; i < k.steps && status == ZERO_OK; ++i) {
         const double usual_coeffs[3] = {3.4445, -4.7750, 2.0315};
