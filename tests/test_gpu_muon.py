@@ -327,9 +327,11 @@ def test_the_binding_refuses_what_does_not_fit():
 
 
 @pytest.mark.parametrize("count,r,c", [(4, 2300, 2500), (5, 2304, 2304), (1, 2900, 5200),
-                                       (2, 200, 9000), (1, 64, 7000), (1, 9000, 64)])
+                                       (2, 200, 9000), (1, 64, 7000), (1, 9000, 64),
+                                       (300, 60, 30), (7, 64, 1024), (2, 1020, 50), (3, 120, 320),
+                                       (3, 310, 100), (2, 65, 321)])
 def test_orthogonalize_large(count, r, c):
-    """tiles of 256 and their quarters, contractions in parts"""
+    """tiles of 256 and their quarters, contractions in parts, many small ones"""
     u = torch.randn(count, r, c, generator=gen(r), device="cuda").to(BF)
     o = torch.empty_like(u)
     zs.zero_orthogonalize(u, o)

@@ -127,6 +127,42 @@ __device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
     lo = FP16::down(v - FP16::up(hi));
 }
 
+// Eight fp16 values in four registers, pair by pair: elements of a 16-bit
+// vector set one by one take a register each on the way.
+using f32x2 = float __attribute__((ext_vector_type(2)));
+using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ f32x2 pair(u32x4 h, int p) {
+    const uint32_t w = h[p];  // a value: the bits of a vector's element are those of its first
+    return __builtin_convertvector(__builtin_bit_cast(f16x2, w), f32x2);
+}
+__device__ __forceinline__ u32x4 pack(const float (&v)[8]) {
+    u32x4 h;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        h[p] = __builtin_bit_cast(
+            uint32_t, __builtin_convertvector(f32x2{v[2 * p], v[2 * p + 1]}, f16x2));
+    return h;
+}
+__device__ __forceinline__ void split8(const float (&v)[8], u32x4 &hi, u32x4 &lo) {
+    hi = pack(v);
+    float rest[8];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const f32x2 h = pair(hi, p);
+        rest[2 * p] = v[2 * p] - h[0];
+        rest[2 * p + 1] = v[2 * p + 1] - h[1];
+    }
+    lo = pack(rest);
+}
+
+// kScale / (sqrt(s) + eps); NaN where a matrix has an Inf or a NaN, which is
+// then NaN throughout
+__device__ __forceinline__ double scale_of(double s, double eps) {
+    const double norm = sqrt(s) + eps;
+    return norm - norm == 0.0 ? static_cast<double>(kScale) / norm : norm - norm;
+}
+
 template <int DT, bool TALL>
 __global__ void __launch_bounds__(256) spread_kernel(Input in, const double *parts, double eps,
                                                      uint16_t *hi, uint16_t *lo, int32_t rp,
@@ -139,9 +175,7 @@ __global__ void __launch_bounds__(256) spread_kernel(Input in, const double *par
     if ((t & 63) == 0) wave_part[t >> 6] = s;
     __syncthreads();
     s = ((wave_part[0] + wave_part[1]) + wave_part[2]) + wave_part[3];
-    const double norm = sqrt(s) + eps;
-    // an Inf or a NaN anywhere makes the matrix NaN
-    const double inv = norm - norm == 0.0 ? static_cast<double>(kScale) / norm : norm - norm;
+    const double inv = scale_of(s, eps);
     const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
     const int64_t base = m * in.su;
     if (TALL) {
@@ -595,6 +629,270 @@ __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kerne
 }
 
 // ---------------------------------------------------------------------------
+// Small matrices: one workgroup does all rounds of a matrix, with X (hi), A
+// and P in shared memory; only lo goes through the workspace.  The products'
+// launches, seventeen for five rounds, take at least 4 us each.  A call by one
+// workgroup a matrix : by launches, us: 64 x 64 15 : 60, 64 x 512 39 : 73,
+// 64 x 1024 69 : 84 (its transpose 91 : 85), 128 x 128 44 : 70, 128 x 320
+// 71 : 75, 48 of 64 x 1024 72 : 125, 1000 of 64 x 64 62 : 596.  A CU's vector
+// units (hi and lo of every element, each round) and its reads of shared
+// memory bound it; longer rows are left to the products, which have all CUs.
+//
+// X and A lie row by row in 16-byte pieces, piece s of row i at s ^ tw(i): tw
+// differs for any eight rows in turn, and among four of them in the units of
+// 32 bytes that the transposing reads take.
+
+__device__ __forceinline__ int tw(int row) { return (row & 3) * 2 | (row >> 2 & 1); }
+__device__ __forceinline__ int piece_of(int row, int ld, int s) {
+    return row * ld + (s ^ tw(row)) * 8;
+}
+
+// a lane's operand, its eight consecutive c of the 32 from c0 on: of 16 rows
+// from row0 on, or (Q) of block f of the rows from row0 on, in the order that
+// leaves a lane eight neighbouring results of two blocks
+template <bool Q>
+__device__ __forceinline__ s16x8 rows_at(const uint16_t *m, int ld, int row0, int f, int c0,
+                                         int lane) {
+    const int t = lane & 15, g = lane >> 4;
+    const int row = row0 + (Q ? (f >> 1) * 32 + (t >> 2) * 8 + (f & 1) * 4 + (t & 3) : f * 16 + t);
+    return *reinterpret_cast<const s16x8 *>(m + piece_of(row, ld, c0 / 8 + g));
+}
+// the same of 16 columns, block f of those from column j0 on, in that order:
+// the rows c0 .. c0 + 31 are the contraction
+__device__ __forceinline__ s16x8 columns_at(const uint16_t *m, int ld, int j0, int f, int c0,
+                                            int lane) {
+    const int t = lane & 15, g = lane >> 4;
+    const int s = j0 / 8 + (f >> 1) * 4 + (t & 3);
+    using lds4 = __attribute__((address_space(3))) s16x4;
+    s16x8 v;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = c0 + g * 8 + h * 4 + (t >> 2);
+        const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds4 *)(m + piece_of(row, ld, s) + (f & 1) * 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[h * 4 + e] = x[e];
+    }
+    return v;
+}
+
+struct SmallArgs {
+    Input in;
+    uint16_t *lo;
+    void *o;
+    int64_t ldo, so;
+    double eps;
+    int32_t cp, steps, tall, bf16;
+    float coeffs[3 * ZERO_NS_MAX_STEPS];
+};
+
+constexpr int kSmallWaves = 8;
+template <int R>
+constexpr int kSmallColumns = R == 64 ? 1024 : 320;  // of the longest rows
+
+template <int DT, int R>
+__global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) {
+    constexpr int THREADS = kSmallWaves * kWave;
+    constexpr int WJ = R / 32, WI = kSmallWaves / WJ, FI = R / WI / 16;
+    __shared__ __attribute__((aligned(128))) uint16_t X[R * kSmallColumns<R>];
+    __shared__ __attribute__((aligned(128))) uint16_t A[R * R];
+    __shared__ float diag[R];
+    __shared__ double wave_part[kSmallWaves];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t m = blockIdx.x, base = m * a.in.su;
+    const int C = a.cp;
+    const int r = a.tall ? a.in.cols : a.in.rows, c = a.tall ? a.in.rows : a.in.cols;
+    uint16_t *lo = a.lo + m * R * C;
+
+    // |U|^2
+    double s = 0.0;
+    {
+        const int a_row = (a.in.cols + 7) / 8, total = a_row * a.in.rows;
+        for (int p = tid; p < total; p += THREADS) {
+            const int i = p / a_row, j = (p - i * a_row) * 8;
+            float v[8];
+            eight<DT>(a.in.u, base + i * a.in.ldu + j, a.in.cols - j, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double d = static_cast<double>(v[e]);
+                s = __builtin_fma(d, d, s);
+            }
+        }
+    }
+    s = wave_sum(s);
+    if (lane == 0) wave_part[wave] = s;
+    __syncthreads();
+    s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kSmallWaves; ++w) s += wave_part[w];
+    const double inv = scale_of(s, a.eps);
+    // X; neighbouring lanes take neighbouring pieces of a row, or (tall) of a
+    // column, whichever are neighbours in memory
+    const int a_row = C / 8;
+    for (int p = tid; p < R * a_row; p += THREADS) {
+        const int i = a.tall ? p % R : p / a_row, j = (a.tall ? p / R : p % a_row) * 8;
+        float v[8];
+        if (a.tall) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = i < r && j + e < c ? element<DT>(a.in.u, base + (j + e) * a.in.ldu + i)
+                                          : 0.0f;
+        } else {
+            eight<DT>(a.in.u, base + i * a.in.ldu + j, i < r ? c - j : 0, v);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = i < r && j + e < c ? static_cast<float>(static_cast<double>(v[e]) * inv) : 0.0f;
+        u32x4 h, l;
+        split8(v, h, l);
+        *reinterpret_cast<u32x4 *>(X + piece_of(i, C, j / 8)) = h;
+        *reinterpret_cast<u32x4 *>(lo + i * C + j) = l;
+    }
+    __syncthreads();
+
+    const int wi = wave / WJ * (R / WI), wj = wave % WJ * 32;
+#pragma unroll 1
+    for (int step = 0; step < a.steps; ++step) {
+        const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1],
+                    cc = a.coeffs[3 * step + 2];
+        f32x4 acc[FI][2];
+        // the products of 64 of the contraction, the loads of all first
+        auto multiply = [&](const uint16_t *mat, int ld, int k) __attribute__((always_inline)) {
+            s16x8 q[2][2], p[2][FI];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    q[h][b] = rows_at<true>(mat, ld, wj, b, k + 32 * h, lane);
+#pragma unroll
+                for (int f = 0; f < FI; ++f)
+                    p[h][f] = rows_at<false>(mat, ld, wi, f, k + 32 * h, lane);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int f = 0; f < FI; ++f)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) acc[f][b] = mfma<FP16>(q[h][b], p[h][f], acc[f][b]);
+        };
+        // A = X X^T: a wave has R / WI x 32 of it
+#pragma unroll
+        for (int f = 0; f < FI; ++f) acc[f][0] = acc[f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int k = 0; k < C; k += 64) multiply(X, C, k);
+        const int j = wj + g * 8;
+        u32x4 own[FI];
+#pragma unroll
+        for (int f = 0; f < FI; ++f) {
+            const int i = wi + f * 16 + (lane & 15);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] = acc[f][e / 4][e & 3];
+                if (i == j + e) diag[i] = v[e] * kInv2;
+                v[e] = i == j + e ? 0.0f : v[e] * kInv;
+            }
+            own[f] = pack(v);
+            *reinterpret_cast<u32x4 *>(A + piece_of(i, R, j / 8)) = own[f];
+            acc[f][0] = acc[f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        __syncthreads();
+        // P = a + b A + c A A
+#pragma unroll
+        for (int k = 0; k < R; k += 64) multiply(A, R, k);
+        float di[FI], dj[8];
+#pragma unroll
+        for (int f = 0; f < FI; ++f) di[f] = diag[wi + f * 16 + (lane & 15)];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dj[e] = diag[j + e];
+        __syncthreads();  // nobody reads A and its diagonal any more
+#pragma unroll
+        for (int f = 0; f < FI; ++f) {
+            const int i = wi + f * 16 + (lane & 15);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float oo = acc[f][e / 4][e & 3] * kInv2;
+                const float oij = pair(own[f], e / 2)[e & 1] * kInv;
+                const float sq = __builtin_fmaf(di[f] + dj[e], oij, oo);
+                if (i == j + e) diag[i] = ca + cb * di[f] + cc * (oo + di[f] * di[f]);
+                v[e] = i == j + e ? 0.0f : __builtin_fmaf(cc, sq, cb * oij) * kScale;
+            }
+            *reinterpret_cast<u32x4 *>(A + piece_of(i, R, j / 8)) = pack(v);
+        }
+        __syncthreads();
+        // X = P X: a wave has all rows of 32 columns at a time, and is the only
+        // one to read and to write them
+#pragma unroll 1
+        for (int j0 = wave * 32; j0 < C; j0 += kSmallWaves * 32) {
+            const int j = j0 + g * 8;
+            u32x4 l[R / 16];
+#pragma unroll
+            for (int f = 0; f < R / 16; ++f)
+                l[f] = *reinterpret_cast<const u32x4 *>(lo + (f * 16 + (lane & 15)) * C + j);
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 x[R / 16][2];
+#pragma unroll
+            for (int f = 0; f < R / 16; ++f) x[f][0] = x[f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int k = 0; k < R; k += 64) {
+                s16x8 q[2][2], p[2][R / 16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        q[h][b] = columns_at(X, C, j0, b, k + 32 * h, lane);
+#pragma unroll
+                    for (int f = 0; f < R / 16; ++f)
+                        p[h][f] = rows_at<false>(A, R, 0, f, k + 32 * h, lane);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int f = 0; f < R / 16; ++f)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) x[f][b] = mfma<FP16>(q[h][b], p[h][f], x[f][b]);
+            }
+#pragma unroll
+            for (int f = 0; f < R / 16; ++f) {
+                __builtin_amdgcn_sched_barrier(0);
+                const int i = f * 16 + (lane & 15);
+                uint16_t *xp = X + piece_of(i, C, j / 8);
+                const u32x4 h = *reinterpret_cast<const u32x4 *>(xp);
+                const float e_i = diag[i];
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = __builtin_fmaf(
+                        e_i, pair(h, e / 2)[e & 1] + pair(l[f], e / 2)[e & 1],
+                        x[f][e / 4][e & 3] * kInv);
+                if (step + 1 < a.steps) {
+                    u32x4 nh, nl;
+                    split8(v, nh, nl);
+                    *reinterpret_cast<u32x4 *>(xp) = nh;
+                    *reinterpret_cast<u32x4 *>(lo + i * C + j) = nl;
+                } else if (i < r) {
+                    uint16_t *o = static_cast<uint16_t *>(a.o) + m * a.so;
+                    u16x8 y;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = a.bf16 ? BF16::down(v[e] * kInv) : FP16::down(v[e] * kInv);
+                    if (!a.tall && j + 8 <= c) {
+                        __builtin_memcpy(o + i * a.ldo + j, &y, 16);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (j + e < c) o[a.tall ? (j + e) * a.ldo + i : i * a.ldo + j + e] = y[e];
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
 // host
 
 inline int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
@@ -734,6 +1032,19 @@ void spread(const Input &in, const Work &w, int64_t count, double eps, char *ws,
         spread_kernel<DT, false><<<grid, 256, 0, st>>>(in, parts, eps, hi, lo, rp, cp);
 }
 
+bool is_small(const Work &w) {
+    return w.rp == 64 ? w.cp <= kSmallColumns<64> : w.rp == 128 && w.cp <= kSmallColumns<128>;
+}
+
+template <int DT>
+void run_small(const SmallArgs &a, int64_t rp, int64_t count, hipStream_t st) {
+    const uint32_t n = static_cast<uint32_t>(count);
+    if (rp == 64)
+        small_kernel<DT, 64><<<n, kSmallWaves * kWave, 0, st>>>(a);
+    else
+        small_kernel<DT, 128><<<n, kSmallWaves * kWave, 0, st>>>(a);
+}
+
 // a stack of count matrices: the span of all, and whether its strides hold
 bool stack_ok(const Mat &one, int64_t count, int64_t stride, Span *all) {
     if (!one.ok()) return false;
@@ -786,6 +1097,21 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     char *ws = static_cast<char *>(workspace);
     const bool tall = rows > cols;
     const Input in{u, ldu, su, static_cast<int32_t>(rows), static_cast<int32_t>(cols)};
+    const double usual_coeffs[3] = {3.4445, -4.7750, 2.0315};
+    if (is_small(w)) {
+        SmallArgs a{in, reinterpret_cast<uint16_t *>(ws + w.lo), o, ldo, so, k.eps,
+                    static_cast<int32_t>(w.cp), k.steps, tall, odt == ZERO_BF16, {}};
+        for (int i = 0; i < 3 * k.steps; ++i)
+            a.coeffs[i] =
+                static_cast<float>(k.coeffs != nullptr ? k.coeffs[i] : usual_coeffs[i % 3]);
+        if (udt == ZERO_BF16)
+            run_small<ZERO_BF16>(a, w.rp, count, st);
+        else if (udt == ZERO_FP16)
+            run_small<ZERO_FP16>(a, w.rp, count, st);
+        else
+            run_small<ZERO_FP32>(a, w.rp, count, st);
+        return launch_status();
+    }
     if (udt == ZERO_BF16)
         spread<ZERO_BF16>(in, w, count, k.eps, ws, tall, st);
     else if (udt == ZERO_FP16)
@@ -813,7 +1139,6 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     base.partial = reinterpret_cast<f32x4 *>(ws + w.partial);
     zero_status status = launch_status();
     for (int i = 0; i < k.steps && status == ZERO_OK; ++i) {
-        const double usual_coeffs[3] = {3.4445, -4.7750, 2.0315};
         const double *c = k.coeffs != nullptr ? k.coeffs + 3 * i : usual_coeffs;
         const uint16_t *x = hi[i & 1];
         Args g = base;
