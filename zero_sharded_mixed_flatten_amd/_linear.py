@@ -108,6 +108,17 @@ def _odd_mat(t, what, shape, dtype, dev):
     return t.data_ptr(), (s0 if r > 1 else max(c, 1))
 
 
+def _vec(t, what, need, dtype, dev):
+    """Address of a contiguous GPU tensor of at least `need` elements of this
+    type on device number dev (None -> NULL)."""
+    if t is None:
+        return None
+    if t.is_cuda and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and \
+            t.numel() >= need:
+        return t.data_ptr()
+    return _buf(t, what, need, dtype, torch.device("cuda", dev)).value  # the refusal
+
+
 def _shape(t, what):
     """a matrix argument's own shape and device number"""
     if not getattr(t, "is_cuda", False):

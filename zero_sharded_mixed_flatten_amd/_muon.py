@@ -12,9 +12,9 @@ import ctypes
 
 import torch
 
-from . import (ZeroValueError, ZERO_EINVAL, _buf, _consts, _lib, _slot_end, _rows, _dtype_code,
+from . import (ZeroValueError, ZERO_EINVAL, _consts, _dtype_code, _lib, _rows, _slot_end,
                _StepControl)
-from ._linear import _CODE, _call, _in_type, _scratch_of
+from ._linear import _CODE, _call, _in_type, _scratch_of, _vec
 
 ZERO_NS_MAX_STEPS = 32
 
@@ -45,19 +45,30 @@ def _declare(L):
 _declare(_lib)
 
 
+def _code(t, what):
+    """the type code of a bf16, fp16 or fp32 tensor"""
+    code = _CODE.get(getattr(t, "dtype", None))
+    return _dtype_code(t, what, True) if code is None else code
+
+
+def _device(t, what):
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{what}: a GPU tensor is required")
+    return t.get_device()
+
+
 def _momentum(fn, what, grads, n_rows, ld, length, mom, u, consts, nesterov, skip, sumsq, max_norm,
               loss_scale, stream):
-    d = mom.device
+    dev = _device(mom, "mom")
     ctl = None
     if skip is not None or sumsq is not None or loss_scale is not None:
         ctl = ctypes.byref(_StepControl(
-            _buf(skip, "skip", 1, torch.int32, d), _buf(sumsq, "sumsq", 1, torch.float64, d),
-            float(max_norm), _buf(loss_scale, "loss_scale", 2, torch.int32, d)))
-    pm = _buf(mom, "mom", length, torch.float32)
-    pg = _rows(grads, "grads", n_rows, ld, length, device=d)
-    pu = _buf(u, "u", length, device=d)
-    _call(fn, what, mom.get_device(), stream, pg, _dtype_code(grads, "grads", True), n_rows, ld,
-          length, pm, pu, _dtype_code(u, "u", True), int(bool(nesterov)), consts, ctl)
+            _vec(skip, "skip", 1, torch.int32, dev), _vec(sumsq, "sumsq", 1, torch.float64, dev),
+            float(max_norm), _vec(loss_scale, "loss_scale", 2, torch.int32, dev)))
+    gc, uc = _code(grads, "grads"), _code(u, "u")
+    _call(fn, what, dev, stream, _rows(grads, "grads", n_rows, ld, length, device=mom.device), gc,
+          n_rows, ld, length, _vec(mom, "mom", length, torch.float32, dev),
+          _vec(u, "u", length, u.dtype, dev), uc, int(bool(nesterov)), consts, ctl)
 
 
 def zero_muon_momentum(grads, n_rows: int, ld: int, length: int, mom, u, hp,
@@ -148,15 +159,15 @@ def zero_orthogonalize(u, o, steps: int = 5, coeffs=None, eps: float = 1e-7, str
 
 def _update(fn, what, o, master, weight_full, layout, rank, consts, update_scale, shard_off,
             length, skip, stream):
+    dev = _device(master, "master")
     if length is None:
         length = master.numel()
-    d = master.device
-    pm = _buf(master, "master", length, torch.float32)
-    _call(fn, what, master.get_device(), stream, _buf(o, "o", length, device=d),
-          _CODE[_in_type(o, "o")], pm,
-          _buf(weight_full, "weight_full", _slot_end(layout, rank, shard_off, length), device=d),
-          _dtype_code(weight_full, "weight_full"), ctypes.byref(layout), rank, shard_off, length,
-          consts, float(update_scale), _buf(skip, "skip", 1, torch.int32, d))
+    ot, wt = _in_type(o, "o"), _in_type(weight_full, "weight_full")
+    _call(fn, what, dev, stream, _vec(o, "o", length, ot, dev), _CODE[ot],
+          _vec(master, "master", length, torch.float32, dev),
+          _vec(weight_full, "weight_full", _slot_end(layout, rank, shard_off, length), wt, dev),
+          _CODE[wt], ctypes.byref(layout), rank, shard_off, length, consts, update_scale,
+          _vec(skip, "skip", 1, torch.int32, dev))
 
 
 def zero_muon_update(o, master, weight_full, layout, rank: int, hp, update_scale: float = 1.0,

@@ -14,8 +14,8 @@ import ctypes
 
 import torch
 
-from . import _buf, _lib
-from ._linear import _CODE, _call, _in_type, _mat, _out_type, _scratch_of, _shape
+from . import _lib
+from ._linear import _CODE, _call, _in_type, _mat, _out_type, _scratch_of, _shape, _vec
 
 
 def _declare(L):
@@ -55,10 +55,9 @@ def zero_layernorm(x, w, b, y, eps: float = 1e-5, mean=None, rstd=None, stream=N
     xt, yt, dev = _out_type(x, dt, "x"), _out_type(y, dt, "y"), x.get_device()
     px, ldx = _mat(x, "x", (m, n), xt, dev)
     py, ldy = _mat(y, "y", (m, n), yt, dev)
-    d = x.device
     _call(_lib.zero_layernorm, "zero_layernorm", dev, stream, px, _CODE[xt], ldx,
-          _buf(w, "w", n, dt, d), _buf(b, "b", n, dt, d), _CODE[dt], m, n, eps, py, _CODE[yt], ldy,
-          _buf(mean, "mean", m, torch.float32, d), _buf(rstd, "rstd", m, torch.float32, d))
+          _vec(w, "w", n, dt, dev), _vec(b, "b", n, dt, dev), _CODE[dt], m, n, eps, py, _CODE[yt],
+          ldy, _vec(mean, "mean", m, torch.float32, dev), _vec(rstd, "rstd", m, torch.float32, dev))
 
 
 def zero_layernorm_workspace_bytes(m: int, n: int) -> int:
@@ -81,7 +80,7 @@ def zero_layernorm_backward(dy, x, w, mean, rstd, dx, residual=None, dw=None, db
     of zero_layernorm_workspace_bytes(m, n) bytes is passed."""
     m, n = _shape(x, "x")
     dt = _weight_type(w, None, x, dy)
-    xt, yt, dev, d = _out_type(x, dt, "x"), _out_type(dy, dt, "dy"), x.get_device(), x.device
+    xt, yt, dev = _out_type(x, dt, "x"), _out_type(dy, dt, "dy"), x.get_device()
     gt = torch.float32 if dw is None and db is None else \
         _out_type(dw if dw is not None else db, dt, "dw" if dw is not None else "db")
     px, ldx = _mat(x, "x", (m, n), xt, dev)
@@ -89,9 +88,9 @@ def zero_layernorm_backward(dy, x, w, mean, rstd, dx, residual=None, dw=None, db
     pd, lddx = _mat(dx, "dx", (m, n), xt, dev)
     pr, ldr = (None, n) if residual is None else _mat(residual, "residual", (m, n), xt, dev)
     need = 0 if dw is None and db is None else zero_layernorm_workspace_bytes(m, n)
-    held, ws, nb = _scratch_of(need, workspace, stream, d)
+    held, ws, nb = _scratch_of(need, workspace, stream, x.device)
     _call(_lib.zero_layernorm_backward, "zero_layernorm_backward", dev, stream, py, _CODE[yt],
-          lddy, px, _CODE[xt], ldx, _buf(w, "w", n, dt, d), _CODE[dt],
-          _buf(mean, "mean", m, torch.float32, d), _buf(rstd, "rstd", m, torch.float32, d), m, n,
-          pr, ldr, pd, lddx, _buf(dw, "dw", n, gt, d), _buf(db, "db", n, gt, d), _CODE[gt],
+          lddy, px, _CODE[xt], ldx, _vec(w, "w", n, dt, dev), _CODE[dt],
+          _vec(mean, "mean", m, torch.float32, dev), _vec(rstd, "rstd", m, torch.float32, dev), m,
+          n, pr, ldr, pd, lddx, _vec(dw, "dw", n, gt, dev), _vec(db, "db", n, gt, dev), _CODE[gt],
           int(bool(accumulate)), ws, nb)
