@@ -262,13 +262,13 @@ __device__ __forceinline__ P *uniform(P *p) {
 // A gram product of few tiles and a long contraction is divided into a.parts
 // of it (blockIdx.y), whose fp32 sums lie in the workspace as the lanes hold
 // them; JOIN, a second launch, adds them in their order.
-template <int KIND, int BT, int WI, int WJ, int KG, bool JOIN = false>
+template <int KIND, int BT, int WI, int WJ, int KG, int ST, bool JOIN = false>
 __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kernel(Args a) {
     constexpr bool SYM = KIND == GRAM || KIND == SQUARE, QKC = SYM;
     constexpr int THREADS = WI * WJ * kWave;
     constexpr int FI = BT / WI / 16, FJ = BT / WJ / 16;
     constexpr int SLOT = kTile<true, BT> + kTile<QKC, BT>;
-    __shared__ __attribute__((aligned(1024))) uint16_t all_tiles[KG * 2 * SLOT];
+    __shared__ __attribute__((aligned(1024))) uint16_t all_tiles[KG * ST * SLOT];
 
     const bool quarters = BT == 128 && a.quarter >= 0;
     const int id = quarters ? a.quarter + static_cast<int>(blockIdx.x >> 2)
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kerne
     const int any_wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     const int kg = any_wave / (WI * WJ), wave = any_wave % (WI * WJ);
     const int wi = wave / WJ * (BT / WI), wj = wave % WJ * (BT / WJ);
-    uint16_t *tiles = all_tiles + kg * 2 * SLOT;
+    uint16_t *tiles = all_tiles + kg * ST * SLOT;
     const int i0 = ti * BT, j0 = tj * BT;
     const int nj = SYM ? a.rp : a.cp, nc = KIND == GRAM ? a.cp : a.rp;
     const int64_t px = static_cast<int64_t>(m) * a.rp * a.cp;
@@ -354,7 +354,9 @@ __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kerne
     dq.stride *= KG;
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t *)tiles));
-    auto slot_of = [&](int s) __attribute__((always_inline)) { return (s & 1) * SLOT; };
+    auto slot_of = [&](int s) __attribute__((always_inline)) {
+        return (s & (ST - 1)) * SLOT;
+    };
     auto copy = [&](int n, int s) __attribute__((always_inline)) {
         if (n < NP)
             dp.issue(n, lds + 2 * slot_of(s), wave);
@@ -404,53 +406,57 @@ __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kerne
     };
     using first_half = std::integral_constant<int, 0>;
     using second_half = std::integral_constant<int, 1>;
-    auto arrive = [&]() __attribute__((always_inline)) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // this wave's reads are done and all but the last `flying` of its copies
+    // have landed
+    auto arrive = [&](auto flying) __attribute__((always_inline)) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(flying)::value) : "memory");
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
+    using none = std::integral_constant<int, 0>;
+    constexpr int EACH_STEP = NP + NQ;
     // this group's steps; the groups meet at every barrier, also those that
     // have none left
     const int total = KIND == GRAM ? min(a.part_steps, nc / kBK - c0 / kBK) : nc / kBK;
     const int most = (total + KG - 1) / KG;
     const int steps = KG == 1 ? total : (total - kg + KG - 1) / KG;
-    if (steps > 0) {
 #pragma unroll
-        for (int n = 0; n < NP + NQ; ++n) copy(n, 0);
-        copied();
-    }
-    arrive();
-    if (steps > 1) {
+    for (int t = 0; t < ST; ++t)
+        if (t < steps) {
 #pragma unroll
-        for (int n = 0; n < NP + NQ; ++n) copy(n, 1);
-        copied();
-    }
+            for (int n = 0; n < EACH_STEP; ++n) copy(n, t);
+            copied();
+        }
+    if (steps >= ST)
+        arrive(std::integral_constant<int, (ST - 1) * EACH_STEP>{});
+    else
+        arrive(none{});
 #pragma unroll
     for (int n = 0; n < FI + FJ; ++n) read(n, 0, 0);
     int s = 0;
 #pragma unroll 1
-    for (; s < steps - 2; ++s) {
+    for (; s < steps - ST; ++s) {
         half(first_half{}, std::false_type{}, s, 0);
-        arrive();
-        half(second_half{}, std::true_type{}, s + 1, s + 2);
+        arrive(std::integral_constant<int, (ST - 2) * EACH_STEP>{});
+        half(second_half{}, std::true_type{}, s + 1, s + ST);
         copied();
     }
 #pragma unroll 1
     for (; s < steps; ++s) {
         half(first_half{}, std::false_type{}, s, 0);
-        arrive();
+        arrive(none{});
         half(second_half{}, std::false_type{}, s + 1, 0);
     }
     if constexpr (KG > 1) {
-        if (steps < most) arrive();  // one step fewer, at most
+        if (steps < most) arrive(none{});  // one step fewer, at most
         // each group has a share of the units to finish: the others' sums of
         // these come through the buffers, which nobody reads any more
-        static_assert(FI % KG == 0 && (KG - 1) * 4 * BT * BT <= KG * 4 * SLOT, "the sums fit");
+        static_assert(FI % KG == 0 && (KG - 1) * 2 * BT * BT <= KG * ST * SLOT, "the sums fit");
         f32x4 *sums = reinterpret_cast<f32x4 *>(all_tiles);
         constexpr int EACH = FI / KG * FJ * WI * WJ * kWave;  // of one group's share
-        arrive();
+        arrive(none{});
 #pragma unroll
         for (int f = 0; f < FI; ++f) {
             const int to = f / (FI / KG);
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kerne
                 sums[slot * EACH + ((f % (FI / KG) * FJ + t) * WI * WJ + wave) * kWave + lane] =
                     acc[f][t];
         }
-        arrive();
+        arrive(none{});
 #pragma unroll
         for (int f = 0; f < FI; ++f) {
             if (f / (FI / KG) != kg) continue;
@@ -941,25 +947,38 @@ int64_t tiles_of(int kind, const Work &w, int64_t bt) {
     return kind == GRAM || kind == SQUARE ? ti * (ti + 1) / 2 : ti * ceil_div(w.cp, bt);
 }
 
-// How a product runs: the side of its tiles, groups of waves a workgroup, and
-// (gram) parts of the contraction.
+// How a product runs: the side of its tiles, groups of waves a workgroup,
+// buffers of steps, and (gram) parts of the contraction.
 struct Way {
-    int side, groups, parts;
+    int side, groups, buffers, parts;
     int64_t steps;  // of a part
 };
 
-Way plan_of(int kind, const Work &w, int64_t count) {
+// Tiles of 256 from half a round of the CUs on.  Fewer are as many smaller
+// ones; one step of the contraction is then over sooner than the next one's
+// copies take, so the smallest tiles have four buffers while two workgroups on
+// each CU are enough for all, and tiles of 128 two groups of waves while one
+// is.  Times of gram, square and apply (us) of one matrix, with
+//                  64, 2 buffers   64, 4 buffers   128, 1 group    128, 2 groups
+//   512 x 512      6.8  7.6  7.3   5.7  6.4  6.4  11.3 12.5 11.9   9.2 10.6 11.4
+//   1024 x 1024   11.1 11.7 11.4   6.9  8.4  9.3  15.4 17.9 17.1  13.0 15.6 15.4
+//   1600 x 1600   15.4 16.4 21.0  12.6 13.3 23.4  21.3 22.9 24.4  19.6 18.0 21.1
+//   2048 x 2048   20.6 21.8 33.0  23.0 24.5 35.0  26.0 27.8 31.8  21.8 23.5 27.9
+// and of a call, tiles of 256 and 128: 3200 x 3200 (91 and 169 tiles of 256)
+// 1060 : 940, 4096 x 4096 (136 and 256) 1530 : 1810.
+//
+// A long contraction of the gram product is divided where its tiles leave CUs
+// idle.  Calls, undivided : divided, us: 128 x 11008 326 : 140, 256 x 8192
+// 264 : 141, 1024 x 4096 256 : 235; 128 x 1024 88 : 93 is left whole.
+Way way_of(int kind, const Work &w, int64_t count) {
     const int64_t steps = (kind == GRAM ? w.cp : w.rp) / kBK;
     const int64_t n256 = count * tiles_of(kind, w, 256), n128 = count * tiles_of(kind, w, 128),
                   n64 = count * tiles_of(kind, w, 64);
-    Way p{64, 1, 1, steps};
-    if (n256 >= 128)
-        p.side = 256;
-    else if (n64 <= 384)
-        p.groups = steps > 2 ? 2 : 1;
-    else if (steps > 8)
-        p = Way{128, n128 <= 256 ? 2 : 1, 1, steps};
-    if (kind == GRAM && p.side == 64) {
+    if (n256 >= kCUs / 2) return Way{256, 1, 2, 1, steps};
+    if (n64 > 2 * kCUs)
+        return steps > 8 ? Way{128, n128 <= kCUs ? 2 : 1, 2, 1, steps} : Way{64, 1, 2, 1, steps};
+    Way p{64, 1, 4, 1, steps};
+    if (kind == GRAM) {
         const int64_t parts = std::min({steps / 8, 384 / n64, int64_t(10)});
         if (parts > 1 && steps - steps / parts > 26) p.steps = ceil_div(steps, parts);
         p.parts = static_cast<int>(ceil_div(steps, p.steps));
@@ -968,13 +987,13 @@ Way plan_of(int kind, const Work &w, int64_t count) {
 }
 
 int64_t partial_bytes(const Work &w, int64_t count) {
-    const Way p = plan_of(GRAM, w, count);
+    const Way p = way_of(GRAM, w, count);
     return p.parts == 1 ? 0 : p.parts * count * tiles_of(GRAM, w, p.side) * p.side * p.side * 4;
 }
 
 template <int KIND>
 zero_status run(Args a, const Work &w, hipStream_t st) {
-    const Way p = plan_of(KIND, w, a.count);
+    const Way p = way_of(KIND, w, a.count);
     const int64_t tiles = tiles_of(KIND, w, p.side), groups = tiles * a.count;
     a.tiles = static_cast<int32_t>(tiles);
     a.tiles_i = static_cast<int32_t>(ceil_div(w.rp, p.side));
@@ -993,25 +1012,25 @@ zero_status run(Args a, const Work &w, hipStream_t st) {
     const uint32_t n = static_cast<uint32_t>(groups - rest);
     const dim3 grid(n, static_cast<uint32_t>(p.parts));
     if (p.side == 256) {
-        product_kernel<KIND, 256, 2, 4, 1><<<grid, 512, 0, st>>>(a);
+        product_kernel<KIND, 256, 2, 4, 1, 2><<<grid, 512, 0, st>>>(a);
         a.quarter = static_cast<int32_t>(groups - rest);
         if (rest > 64)
-            product_kernel<KIND, 128, 2, 2, 1>
+            product_kernel<KIND, 128, 2, 2, 1, 2>
                 <<<static_cast<uint32_t>(4 * rest), 256, 0, st>>>(a);
         else if (rest > 0)
-            product_kernel<KIND, 128, 2, 2, 2>
+            product_kernel<KIND, 128, 2, 2, 2, 2>
                 <<<static_cast<uint32_t>(4 * rest), 512, 0, st>>>(a);
+    } else if (p.side == 128 && p.groups == 1) {
+        product_kernel<KIND, 128, 2, 2, 1, 2><<<grid, 256, 0, st>>>(a);
+    } else if (p.side == 128) {
+        product_kernel<KIND, 128, 2, 2, 2, 2><<<grid, 512, 0, st>>>(a);
+    } else if (p.buffers == 2) {
+        product_kernel<KIND, 64, 2, 2, 1, 2><<<grid, 256, 0, st>>>(a);
+    } else {
+        product_kernel<KIND, 64, 2, 2, 1, 4><<<grid, 256, 0, st>>>(a);
     }
-    else if (p.side == 128 && p.groups == 1)
-        product_kernel<KIND, 128, 2, 2, 1><<<grid, 256, 0, st>>>(a);
-    else if (p.side == 128)
-        product_kernel<KIND, 128, 2, 2, 2><<<grid, 512, 0, st>>>(a);
-    else if (p.groups == 1)
-        product_kernel<KIND, 64, 2, 2, 1><<<grid, 256, 0, st>>>(a);
-    else
-        product_kernel<KIND, 64, 2, 2, 2><<<grid, 512, 0, st>>>(a);
     if constexpr (KIND == GRAM) {
-        if (p.parts > 1) product_kernel<GRAM, 64, 2, 2, 1, true><<<n, 256, 0, st>>>(a);
+        if (p.parts > 1) product_kernel<GRAM, 64, 2, 2, 1, 2, true><<<n, 256, 0, st>>>(a);
     }
     return launch_status();
 }
@@ -1085,7 +1104,7 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     const Work w = work_of(count, rows, cols);
     // a launch has less than 2^32 threads
     for (int kind : {GRAM, SQUARE, APPLY}) {
-        const Way p = plan_of(kind, w, count);
+        const Way p = way_of(kind, w, count);
         if (count * tiles_of(kind, w, p.side) * p.parts >= kMaxTiles) return ZERO_EINVAL;
     }
     if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < w.bytes)
