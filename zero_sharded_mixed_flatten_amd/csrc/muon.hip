@@ -181,6 +181,15 @@ template <class F>
 void for_launches(int64_t len, F f) {
     for (int64_t at = 0; at < len; at += kLaunchElems) f(at, std::min(kLaunchElems, len - at));
 }
+// Waves on a CU: the more a lane has in flight, the fewer keep HBM busiest.
+// Times over 45 M elements (us): 8 bf16 rows 8 waves 192, 12 176, 16 179,
+// uncapped 187; 8 fp32 rows (half of it) 8 147, 12 150, uncapped 155; 64 bf16
+// rows (a quarter) 8 282, 12 256, uncapped 268; one fp32 row 12 113, 16 107,
+// uncapped 112; 2 bf16 rows 16 99, 20 95, uncapped 97; update 16 83, 20 81,
+// uncapped 82.  Short ranges are over before it matters.
+inline size_t residency(int waves, int64_t len) {
+    return len < (int64_t(1) << 20) ? 0 : residency_lds_bytes(waves, kWave);
+}
 inline uint32_t groups_of(int64_t len) {
     return static_cast<uint32_t>((len + kWave * kQuad - 1) / (kWave * kQuad));
 }
@@ -190,8 +199,11 @@ void run_momentum(const void *grads, int64_t ld, int32_t n_rows, int64_t len, fl
                   int32_t nesterov, const Consts &c, const Control &k, hipStream_t st) {
     const auto *g = static_cast<const typename GradT<GDT>::elem *>(grads);
     auto *out = static_cast<typename GradT<UDT>::elem *>(u);
+    const int waves = GDT == ZERO_FP32 ? (n_rows >= 8 ? 8 : 16)
+                                       : (n_rows >= 8 ? 12 : n_rows == 1 ? 16 : 20);
+    const size_t lds = residency(waves, len);
     for_launches(len, [&](int64_t at, int64_t n) {
-        momentum_kernel<GDT, UDT, NDP><<<groups_of(n), kWave, 0, st>>>(
+        momentum_kernel<GDT, UDT, NDP><<<groups_of(n), kWave, lds, st>>>(
             g + at, ld, n_rows, n, mom + at, out + at, nesterov != 0, c, k);
     });
 }
@@ -260,9 +272,10 @@ zero_status momentum_impl(const void *grads, zero_dtype gdt, int32_t n_rows, int
 template <int ODT, int WDT>
 void run_update(const uint16_t *o, int64_t len, float *w, uint16_t *slot, float scale,
                 const Consts &c, const Control &k, hipStream_t st) {
+    const size_t lds = residency(20, len);
     for_launches(len, [&](int64_t at, int64_t n) {
         update_kernel<ODT, WDT>
-            <<<groups_of(n), kWave, 0, st>>>(o + at, n, w + at, slot + at, scale, c, k);
+            <<<groups_of(n), kWave, lds, st>>>(o + at, n, w + at, slot + at, scale, c, k);
     });
 }
 
