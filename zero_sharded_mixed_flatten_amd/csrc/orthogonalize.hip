@@ -682,6 +682,89 @@ __device__ __forceinline__ s16x8 columns_at(const uint16_t *m, int ld, int j0, i
     return v;
 }
 
+constexpr int kSmallWaves = 8;
+
+// What eight waves hold of A, [R][R], and make of it: a wave has R / WI rows
+// of 32 columns, a lane eight neighbouring elements (i, j..j+7) of FI rows.
+template <int R>
+struct Square {
+    static constexpr int WJ = R / 32, WI = kSmallWaves / WJ, FI = R / WI / 16;
+    f32x4 acc[FI][2];
+    u32x4 own[FI];
+    int lane, wi, wj, j;
+    __device__ __forceinline__ Square(int wave, int lane_)
+        : lane(lane_), wi(wave / WJ * (R / WI)), wj(wave % WJ * 32), j(wj + (lane_ >> 4) * 8) {}
+    __device__ __forceinline__ int row(int f) const { return wi + f * 16 + (lane & 15); }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int f = 0; f < FI; ++f) acc[f][0] = acc[f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    // adds the products of m's rows over 64 of the contraction, from k on; the
+    // loads of all first
+    __device__ __forceinline__ void multiply(const uint16_t *m, int ld, int k) {
+        s16x8 q[2][2], p[2][FI];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) q[h][b] = rows_at<true>(m, ld, wj, b, k + 32 * h, lane);
+#pragma unroll
+            for (int f = 0; f < FI; ++f)
+                p[h][f] = rows_at<false>(m, ld, wi, f, k + 32 * h, lane);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int f = 0; f < FI; ++f)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) acc[f][b] = mfma<FP16>(q[h][b], p[h][f], acc[f][b]);
+    }
+    // acc is X X^T: its diagonal to diag, the rest to A in shared memory
+    __device__ __forceinline__ void put(uint16_t *A, float *diag) {
+#pragma unroll
+        for (int f = 0; f < FI; ++f) {
+            const int i = row(f);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] = acc[f][e / 4][e & 3];
+                if (i == j + e) diag[i] = v[e] * kInv2;
+                v[e] = i == j + e ? 0.0f : v[e] * kInv;
+            }
+            own[f] = pack(v);
+            *reinterpret_cast<u32x4 *>(A + piece_of(i, R, j / 8)) = own[f];
+        }
+    }
+    // A and its diagonal become P = a + b A + c A A and its diagonal; all waves
+    // see A before, and P after it
+    __device__ __forceinline__ void polynomial(uint16_t *A, float *diag, float ca, float cb,
+                                               float cc) {
+        clear();
+#pragma unroll
+        for (int k = 0; k < R; k += 64) multiply(A, R, k);
+        float di[FI], dj[8];
+#pragma unroll
+        for (int f = 0; f < FI; ++f) di[f] = diag[row(f)];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dj[e] = diag[j + e];
+        __syncthreads();  // nobody reads A and its diagonal any more
+#pragma unroll
+        for (int f = 0; f < FI; ++f) {
+            const int i = row(f);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float oo = acc[f][e / 4][e & 3] * kInv2;
+                const float oij = pair(own[f], e / 2)[e & 1] * kInv;
+                const float sq = __builtin_fmaf(di[f] + dj[e], oij, oo);
+                if (i == j + e) diag[i] = ca + cb * di[f] + cc * (oo + di[f] * di[f]);
+                v[e] = i == j + e ? 0.0f : __builtin_fmaf(cc, sq, cb * oij) * kScale;
+            }
+            *reinterpret_cast<u32x4 *>(A + piece_of(i, R, j / 8)) = pack(v);
+        }
+        __syncthreads();
+    }
+};
+
 struct SmallArgs {
     Input in;
     uint16_t *lo;
@@ -692,14 +775,12 @@ struct SmallArgs {
     float coeffs[3 * ZERO_NS_MAX_STEPS];
 };
 
-constexpr int kSmallWaves = 8;
 template <int R>
 constexpr int kSmallColumns = R == 64 ? 1024 : 320;  // of the longest rows
 
 template <int DT, int R>
 __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) {
     constexpr int THREADS = kSmallWaves * kWave;
-    constexpr int WJ = R / 32, WI = kSmallWaves / WJ, FI = R / WI / 16;
     __shared__ __attribute__((aligned(128))) uint16_t X[R * kSmallColumns<R>];
     __shared__ __attribute__((aligned(128))) uint16_t A[R * R];
     __shared__ float diag[R];
@@ -757,77 +838,16 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
     }
     __syncthreads();
 
-    const int wi = wave / WJ * (R / WI), wj = wave % WJ * 32;
+    Square<R> square(wave, lane);
 #pragma unroll 1
     for (int step = 0; step < a.steps; ++step) {
-        const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1],
-                    cc = a.coeffs[3 * step + 2];
-        f32x4 acc[FI][2];
-        // the products of 64 of the contraction, the loads of all first
-        auto multiply = [&](const uint16_t *mat, int ld, int k) __attribute__((always_inline)) {
-            s16x8 q[2][2], p[2][FI];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    q[h][b] = rows_at<true>(mat, ld, wj, b, k + 32 * h, lane);
-#pragma unroll
-                for (int f = 0; f < FI; ++f)
-                    p[h][f] = rows_at<false>(mat, ld, wi, f, k + 32 * h, lane);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int f = 0; f < FI; ++f)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) acc[f][b] = mfma<FP16>(q[h][b], p[h][f], acc[f][b]);
-        };
-        // A = X X^T: a wave has R / WI x 32 of it
-#pragma unroll
-        for (int f = 0; f < FI; ++f) acc[f][0] = acc[f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        square.clear();
 #pragma unroll 1
-        for (int k = 0; k < C; k += 64) multiply(X, C, k);
-        const int j = wj + g * 8;
-        u32x4 own[FI];
-#pragma unroll
-        for (int f = 0; f < FI; ++f) {
-            const int i = wi + f * 16 + (lane & 15);
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[e] = acc[f][e / 4][e & 3];
-                if (i == j + e) diag[i] = v[e] * kInv2;
-                v[e] = i == j + e ? 0.0f : v[e] * kInv;
-            }
-            own[f] = pack(v);
-            *reinterpret_cast<u32x4 *>(A + piece_of(i, R, j / 8)) = own[f];
-            acc[f][0] = acc[f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
+        for (int k = 0; k < C; k += 64) square.multiply(X, C, k);
+        square.put(A, diag);
         __syncthreads();
-        // P = a + b A + c A A
-#pragma unroll
-        for (int k = 0; k < R; k += 64) multiply(A, R, k);
-        float di[FI], dj[8];
-#pragma unroll
-        for (int f = 0; f < FI; ++f) di[f] = diag[wi + f * 16 + (lane & 15)];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dj[e] = diag[j + e];
-        __syncthreads();  // nobody reads A and its diagonal any more
-#pragma unroll
-        for (int f = 0; f < FI; ++f) {
-            const int i = wi + f * 16 + (lane & 15);
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float oo = acc[f][e / 4][e & 3] * kInv2;
-                const float oij = pair(own[f], e / 2)[e & 1] * kInv;
-                const float sq = __builtin_fmaf(di[f] + dj[e], oij, oo);
-                if (i == j + e) diag[i] = ca + cb * di[f] + cc * (oo + di[f] * di[f]);
-                v[e] = i == j + e ? 0.0f : __builtin_fmaf(cc, sq, cb * oij) * kScale;
-            }
-            *reinterpret_cast<u32x4 *>(A + piece_of(i, R, j / 8)) = pack(v);
-        }
-        __syncthreads();
+        square.polynomial(A, diag, a.coeffs[3 * step], a.coeffs[3 * step + 1],
+                          a.coeffs[3 * step + 2]);
         // X = P X: a wave has all rows of 32 columns at a time, and is the only
         // one to read and to write them
 #pragma unroll 1
@@ -896,6 +916,106 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
         }
         __syncthreads();
     }
+}
+
+// Up to 128 rows, too long for that: A and P by one workgroup a matrix in one
+// launch, from X itself in chunks that pass through shared memory, or (JOIN)
+// from the gram product's parts.  A launch less a round: 77 x 333 79 -> 71 us,
+// 64 x 2048 82 -> 66.
+constexpr int kChunk = 192;
+
+template <int R, bool JOIN>
+__global__ void __launch_bounds__(kSmallWaves *kWave) narrow_kernel(Args a) {
+    constexpr int THREADS = kSmallWaves * kWave;
+    constexpr int PIECES = kChunk / 8, N = R * PIECES / THREADS;
+    __shared__ __attribute__((aligned(128))) uint16_t X[JOIN ? 8 : R * kChunk];
+    __shared__ __attribute__((aligned(128))) uint16_t A[R * R];
+    __shared__ float diag[R];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t m = blockIdx.x;
+    Square<R> square(wave, lane);
+    if constexpr (JOIN) {
+        // chunks of the lanes' sums as tiles of 64 hold them: two by two waves
+        // of 32 x 32, two by two blocks of 16 x 16 each
+        for (int at = wave; at < a.tiles * 4; at += kSmallWaves) {
+            const int tile = at >> 2, w = at & 3;
+            const int ti = tile == 0 ? 0 : 1, tj = tile == 2 ? 1 : 0;
+            f32x4 sum[2][2];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) sum[f][0] = sum[f][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const f32x4 *p = a.partial + (m * a.tiles + tile) * 1024 + w * kWave + lane;
+#pragma unroll 4
+            for (int part = 0; part < a.parts; ++part) {
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) sum[f][t] += p[(f * 2 + t) * 4 * kWave];
+                p += static_cast<int64_t>(a.count) * a.tiles * 1024;
+            }
+            const int j = tj * 64 + (w & 1) * 32 + (lane >> 4) * 8;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const int i = ti * 64 + (w >> 1) * 32 + f * 16 + (lane & 15);
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[e] = sum[f][e / 4][e & 3];
+                    if (i == j + e) diag[i] = v[e] * kInv2;
+                    v[e] = i == j + e ? 0.0f : v[e] * kInv;
+                }
+                *reinterpret_cast<u32x4 *>(A + piece_of(i, R, j / 8)) = pack(v);
+                if (ti != tj) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        A[piece_of(j + e, R, i / 8) + (i & 7)] = FP16::down(v[e]);
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int f = 0; f < Square<R>::FI; ++f)
+            square.own[f] = *reinterpret_cast<const u32x4 *>(A + piece_of(square.row(f), R,
+                                                                          square.j / 8));
+    } else {
+        const uint16_t *x = a.p + m * R * a.cp;
+        u32x4 next[N];
+        auto load = [&](int c0) __attribute__((always_inline)) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int p = n * THREADS + tid, i = p / PIECES, c = c0 + p % PIECES * 8;
+                // past the row's end its first piece, which is not multiplied
+                next[n] = *reinterpret_cast<const u32x4 *>(x + i * a.cp + (c < a.cp ? c : 0));
+            }
+        };
+        load(0);
+        square.clear();
+#pragma unroll 1
+        for (int c0 = 0; c0 < a.cp; c0 += kChunk) {
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int p = n * THREADS + tid;
+                *reinterpret_cast<u32x4 *>(X + piece_of(p / PIECES, kChunk, p % PIECES)) = next[n];
+            }
+            if (c0 + kChunk < a.cp) load(c0 + kChunk);
+            __syncthreads();
+            const int left = a.cp - c0;
+#pragma unroll
+            for (int k = 0; k < kChunk; k += 64)
+                if (k < left) square.multiply(X, kChunk, k);
+        }
+        square.put(A, diag);
+        __syncthreads();
+    }
+    square.polynomial(A, diag, a.ca, a.cb, a.cc);
+    uint16_t *out = a.out + m * R * R;
+    for (int p = tid; p < R * R / 8; p += THREADS) {
+        const int i = p / (R / 8), s = p % (R / 8);
+        *reinterpret_cast<u32x4 *>(out + p * 8) =
+            *reinterpret_cast<const u32x4 *>(A + piece_of(i, R, s));
+    }
+    if (tid < R) a.new_diag[m * R + tid] = diag[tid];
 }
 
 // ---------------------------------------------------------------------------
@@ -968,19 +1088,25 @@ struct Way {
 // 1060 : 940, 4096 x 4096 (136 and 256) 1530 : 1810.
 //
 // A long contraction of the gram product is divided where its tiles leave CUs
-// idle.  Calls, undivided : divided, us: 128 x 11008 326 : 140, 256 x 8192
-// 264 : 141, 1024 x 4096 256 : 235; 128 x 1024 88 : 93 is left whole.
+// idle.  Calls, undivided : divided, us: 256 x 8192 264 : 141, 1024 x 4096
+// 256 : 235, 128 x 1024 96 : 81, 128 x 2048 137 : 91; 128 x 512 75 : 78 is left
+// whole.
 Way way_of(int kind, const Work &w, int64_t count) {
     const int64_t steps = (kind == GRAM ? w.cp : w.rp) / kBK;
     const int64_t n256 = count * tiles_of(kind, w, 256), n128 = count * tiles_of(kind, w, 128),
                   n64 = count * tiles_of(kind, w, 64);
-    if (n256 >= kCUs / 2) return Way{256, 1, 2, 1, steps};
-    if (n64 > 2 * kCUs)
+    const bool narrow = kind == GRAM && w.rp <= 128;
+    if (n256 >= kCUs / 2 && !narrow) return Way{256, 1, 2, 1, steps};
+    if (n64 > 2 * kCUs && !narrow)
         return steps > 8 ? Way{128, n128 <= kCUs ? 2 : 1, 2, 1, steps} : Way{64, 1, 2, 1, steps};
     Way p{64, 1, 4, 1, steps};
     if (kind == GRAM) {
-        const int64_t parts = std::min({steps / 8, 384 / n64, int64_t(10)});
-        if (parts > 1 && steps - steps / parts > 26) p.steps = ceil_div(steps, parts);
+        // of eight steps and more, or (few rows) of four: what is not divided
+        // there is one workgroup's work
+        const int64_t parts = narrow ? std::min({steps / 4, 384 / n64, int64_t(8)})
+                                     : std::min({steps / 8, 384 / n64, int64_t(10)});
+        if (parts > 1 && (narrow ? steps >= 12 : steps - steps / parts > 26))
+            p.steps = ceil_div(steps, parts);
         p.parts = static_cast<int>(ceil_div(steps, p.steps));
     }
     return p;
@@ -1030,7 +1156,9 @@ zero_status run(Args a, const Work &w, hipStream_t st) {
         product_kernel<KIND, 64, 2, 2, 1, 4><<<grid, 256, 0, st>>>(a);
     }
     if constexpr (KIND == GRAM) {
-        if (p.parts > 1) product_kernel<GRAM, 64, 2, 2, 1, 2, true><<<n, 256, 0, st>>>(a);
+        // up to 128 rows the parts are added by the kernel that squares
+        if (p.parts > 1 && w.rp > 128)
+            product_kernel<GRAM, 64, 2, 2, 1, 2, true><<<n, 256, 0, st>>>(a);
     }
     return launch_status();
 }
@@ -1049,6 +1177,16 @@ void spread(const Input &in, const Work &w, int64_t count, double eps, char *ws,
         spread_kernel<DT, true><<<grid, 256, 0, st>>>(in, parts, eps, hi, lo, rp, cp);
     else
         spread_kernel<DT, false><<<grid, 256, 0, st>>>(in, parts, eps, hi, lo, rp, cp);
+}
+
+void run_narrow(const Args &a, bool join, hipStream_t st) {
+    const uint32_t n = static_cast<uint32_t>(a.count);
+    if (a.rp == 64)
+        join ? narrow_kernel<64, true><<<n, kSmallWaves * kWave, 0, st>>>(a)
+             : narrow_kernel<64, false><<<n, kSmallWaves * kWave, 0, st>>>(a);
+    else
+        join ? narrow_kernel<128, true><<<n, kSmallWaves * kWave, 0, st>>>(a)
+             : narrow_kernel<128, false><<<n, kSmallWaves * kWave, 0, st>>>(a);
 }
 
 bool is_small(const Work &w) {
@@ -1156,6 +1294,7 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     base.tall = tall;
     base.bf16 = odt == ZERO_BF16;
     base.partial = reinterpret_cast<f32x4 *>(ws + w.partial);
+    const Way gram = way_of(GRAM, w, count);
     zero_status status = launch_status();
     for (int i = 0; i < k.steps && status == ZERO_OK; ++i) {
         const double *c = k.coeffs != nullptr ? k.coeffs + 3 * i : usual_coeffs;
@@ -1164,8 +1303,6 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
         g.p = g.q = x;
         g.out = A;
         g.new_diag = d;
-        status = run<GRAM>(g, w, st);
-        if (status != ZERO_OK) break;
         Args s = base;
         s.p = s.q = s.hi = A;
         s.out = Q;
@@ -1174,7 +1311,18 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
         s.ca = static_cast<float>(c[0]);
         s.cb = static_cast<float>(c[1]);
         s.cc = static_cast<float>(c[2]);
-        status = run<SQUARE>(s, w, st);
+        const bool divided = gram.parts > 1;
+        if (w.rp > 128 || divided) status = run<GRAM>(g, w, st);
+        if (status != ZERO_OK) break;
+        if (w.rp > 128) {
+            status = run<SQUARE>(s, w, st);
+        } else {
+            s.p = x;
+            s.tiles = static_cast<int32_t>(tiles_of(GRAM, w, 64));
+            s.parts = gram.parts;
+            run_narrow(s, divided, st);
+            status = launch_status();
+        }
         if (status != ZERO_OK) break;
         Args p = base;
         p.p = Q;
