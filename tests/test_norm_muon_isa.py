@@ -41,7 +41,10 @@ def test_the_products():
     asm = isa._asm(SOURCES[2])
     seen = 0
     for name, body, tail in _kernels(asm):
-        if "product_kernel" not in name:
+        if not any(k in name for k in ("product_kernel", "small_kernel", "narrow_kernel")):
+            continue
+        assert re.search(r"; ScratchSize: (0|24)\b", tail), name  # 24: a row's broken end
+        if "product_kernel" not in name or "Lb1E" in name:  # Lb1: joins parts
             continue
         seen += 1
         assert re.search(r"\bv_mfma_f32_16x16x32_f16\b", body)
