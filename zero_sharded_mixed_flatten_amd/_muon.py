@@ -151,7 +151,8 @@ def zero_orthogonalize(u, o, steps: int = 5, coeffs=None, eps: float = 1e-7, str
             raise ZeroValueError(ZERO_EINVAL, "zero_orthogonalize")
         flat = (ctypes.c_double * len(flat))(*flat)
     ns = _NsParams(steps, 0, eps, None if flat is None else ctypes.addressof(flat))
-    need = _lib.zero_orthogonalize_workspace_bytes(count, rows, cols)
+    need = 0 if workspace is not None else \
+        _lib.zero_orthogonalize_workspace_bytes(count, rows, cols)
     held, ws, nb = _scratch_of(need, workspace, stream, u.device)
     _call(_lib.zero_orthogonalize, "zero_orthogonalize", dev, stream, pu, _CODE[u.dtype], ldu, su,
           count, rows, cols, ctypes.byref(ns), po, _CODE[o.dtype], ldo, so, ws, nb)

@@ -87,7 +87,8 @@ def zero_layernorm_backward(dy, x, w, mean, rstd, dx, residual=None, dw=None, db
     py, lddy = _mat(dy, "dy", (m, n), yt, dev)
     pd, lddx = _mat(dx, "dx", (m, n), xt, dev)
     pr, ldr = (None, n) if residual is None else _mat(residual, "residual", (m, n), xt, dev)
-    need = 0 if dw is None and db is None else zero_layernorm_workspace_bytes(m, n)
+    need = 0 if workspace is not None or (dw is None and db is None) else \
+        zero_layernorm_workspace_bytes(m, n)
     held, ws, nb = _scratch_of(need, workspace, stream, x.device)
     _call(_lib.zero_layernorm_backward, "zero_layernorm_backward", dev, stream, py, _CODE[yt],
           lddy, px, _CODE[xt], ldx, _vec(w, "w", n, dt, dev), _CODE[dt],
