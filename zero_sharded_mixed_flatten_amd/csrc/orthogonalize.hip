@@ -37,7 +37,7 @@ using namespace zero_host;
 using namespace zero_linear_impl;
 
 constexpr float kScale = 4096.0f, kInv = 1.0f / 4096.0f, kInv2 = kInv * kInv;
-constexpr int kParts = 256;  // partial sums of squares a matrix
+constexpr int kParts = 256;  // partial sums of squares a matrix, at most
 constexpr int64_t kMaxSide = 65536, kMaxCount = 65535;
 
 struct Input {
@@ -85,7 +85,7 @@ __device__ __forceinline__ void eight(const void *p, int64_t at, int n, float (&
 }
 
 // ---------------------------------------------------------------------------
-// |U|^2 in kParts fp64 parts a matrix: pieces of eight elements, in turn
+// |U|^2 in up to kParts fp64 parts a matrix: pieces of eight elements, in turn
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
@@ -94,13 +94,13 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) squares_kernel(Input in, double *parts) {
-    __shared__ double wave_part[4];
+__global__ void __launch_bounds__(1024) squares_kernel(Input in, double *parts) {
+    __shared__ double wave_part[16];
     const uint32_t a_row = static_cast<uint32_t>(in.cols + 7) / 8;
     const uint32_t total = a_row * static_cast<uint32_t>(in.rows);
     const int64_t base = static_cast<int64_t>(blockIdx.y) * in.su;
     double s = 0.0;
-    for (uint32_t p = blockIdx.x * 256u + threadIdx.x; p < total; p += kParts * 256u) {
+    for (uint32_t p = blockIdx.x * 1024u + threadIdx.x; p < total; p += gridDim.x * 1024u) {
         const uint32_t i = p / a_row, j = (p - i * a_row) * 8u;
         float v[8];
         eight<DT>(in.u, base + i * in.ldu + j, in.cols - static_cast<int>(j), v);
@@ -113,9 +113,10 @@ __global__ void __launch_bounds__(256) squares_kernel(Input in, double *parts) {
     s = wave_sum(s);
     if ((threadIdx.x & 63) == 0) wave_part[threadIdx.x >> 6] = s;
     __syncthreads();
-    if (threadIdx.x == 0)
-        parts[static_cast<int64_t>(blockIdx.y) * kParts + blockIdx.x] =
-            ((wave_part[0] + wave_part[1]) + wave_part[2]) + wave_part[3];
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 16; ++w) s += wave_part[w];
+        parts[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = s;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -164,14 +165,15 @@ __device__ __forceinline__ double scale_of(double s, double eps) {
 }
 
 template <int DT, bool TALL>
-__global__ void __launch_bounds__(256) spread_kernel(Input in, const double *parts, double eps,
+__global__ void __launch_bounds__(256) spread_kernel(Input in, const double *parts, int32_t n_parts,
+                                                     double eps,
                                                      uint16_t *hi, uint16_t *lo, int32_t rp,
                                                      int32_t cp) {
     __shared__ double wave_part[4];
     __shared__ float block[TALL ? 64 : 1][65];
     const int t = threadIdx.x;
     const int64_t m = blockIdx.z;
-    double s = wave_sum(parts[m * kParts + t]);
+    double s = wave_sum(t < n_parts ? parts[m * n_parts + t] : 0.0);
     if ((t & 63) == 0) wave_part[t >> 6] = s;
     __syncthreads();
     s = ((wave_part[0] + wave_part[1]) + wave_part[2]) + wave_part[3];
@@ -1170,13 +1172,17 @@ void spread(const Input &in, const Work &w, int64_t count, double eps, char *ws,
     auto *hi = reinterpret_cast<uint16_t *>(ws + w.hi0);
     auto *lo = reinterpret_cast<uint16_t *>(ws + w.lo);
     const uint32_t n = static_cast<uint32_t>(count);
-    squares_kernel<DT><<<dim3(kParts, n), 256, 0, st>>>(in, parts);
+    // a piece a thread, more in large matrices
+    const int64_t pieces = in.rows * ceil_div(in.cols, 8);
+    const int32_t n_parts =
+        static_cast<int32_t>(std::min<int64_t>(kParts, ceil_div(pieces, 1024)));
+    squares_kernel<DT><<<dim3(static_cast<uint32_t>(n_parts), n), 1024, 0, st>>>(in, parts);
     const dim3 grid(static_cast<uint32_t>(w.cp / 64), static_cast<uint32_t>(w.rp / 64), n);
     const int32_t rp = static_cast<int32_t>(w.rp), cp = static_cast<int32_t>(w.cp);
     if (tall)
-        spread_kernel<DT, true><<<grid, 256, 0, st>>>(in, parts, eps, hi, lo, rp, cp);
+        spread_kernel<DT, true><<<grid, 256, 0, st>>>(in, parts, n_parts, eps, hi, lo, rp, cp);
     else
-        spread_kernel<DT, false><<<grid, 256, 0, st>>>(in, parts, eps, hi, lo, rp, cp);
+        spread_kernel<DT, false><<<grid, 256, 0, st>>>(in, parts, n_parts, eps, hi, lo, rp, cp);
 }
 
 void run_narrow(const Args &a, bool join, hipStream_t st) {
