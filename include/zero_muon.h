@@ -70,7 +70,7 @@ typedef struct zero_ns_params {
     int32_t steps;        /* 1 <= steps <= ZERO_NS_MAX_STEPS */
     int32_t reserved;     /* zero */
     double eps;           /* finite, >= 0 */
-    const double *coeffs; /* finite, or NULL */
+    const double *coeffs; /* finite as fp32 values, or NULL */
 } zero_ns_params;
 
 /* Bytes of device workspace that zero_orthogonalize needs for count matrices
@@ -98,9 +98,12 @@ ZERO_API int64_t zero_orthogonalize_workspace_bytes(int64_t count, int64_t rows,
  * stay below 1.3).  Inf or NaN in a matrix makes all of that matrix NaN, and
  * no other; a matrix of zeros stays zero where eps > 0 and is NaN where eps
  * is 0.
- * 1 <= count <= 65535 or an empty call, 0 <= rows, cols <= 65536, strides
- * such that a stack spans at most 2^60 elements; su, so >= the matrix's span
- * where count > 1.  An empty matrix is a no-op.
+ * 0 <= count <= 65535, 0 <= rows, cols <= 65536, a stack spans at most 2^60
+ * elements, and a call has less than 2^23 tiles (of 64 x 64 to 256 x 256).  A
+ * matrix occupies its span, from its first element to one past its last, and
+ * su and so are at least that where count > 1; nothing between a row's end and
+ * the next row's start is read or written.  An empty call or matrix is a
+ * no-op.
  * EINVAL: a bad type, a dimension or parameter out of range, a stride below
  * what it spans, a NULL or unaligned pointer, a missing, unaligned or short
  * workspace.  EALIAS: o or the workspace overlaps anything else. */

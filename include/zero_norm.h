@@ -41,7 +41,7 @@ extern "C" {
  *   mean, rstd: fp32[m] each, for the backward pass, or NULL.
  * EINVAL: a bad type, a dimension out of range, a row stride below its row, a
  * NULL pointer to something read or written, a pointer not aligned to its
- * element, an eps that is not finite and > 0, or mean or rstd where n is 0
+ * element, an eps that is not finite and > 0 as an fp32 value, or mean or rstd where n is 0
  * and m is not.  EALIAS: y, mean or rstd overlaps anything else (y == x
  * excepted). */
 ZERO_API zero_status zero_layernorm(const void *x, zero_dtype xdt, int64_t ldx, const void *w,

@@ -74,6 +74,31 @@ def test_momentum(gt, ut, n_rows):
             assert torch.equal(dm_out, before) and not du[:lead].any() and not du[lead + n:].any()
 
 
+def test_momentum_and_update_at_places_that_do_not_match():
+    """each buffer at another element offset: no common alignment"""
+    g = torch.Generator().manual_seed(5)
+    n = 2050
+    for lg, lm, lu in ((0, 1, 2), (3, 0, 1), (1, 2, 0), (2, 255, 7)):
+        grads = (torch.randn(lg + 3 * n, generator=g) * 1e-3).to(BF)
+        mom = torch.randn(lm + n, generator=g) * 1e-2
+        hp = zs.AdamWHParams(beta1=0.95, grad_scale=1 / 3, lr=0.02)
+        m, u = momentum_cpu(grads[lg:].view(3, n), mom[lm:], hp, True)
+        dm, du = mom.cuda(), torch.zeros(lu + n + 1, dtype=HF, device="cuda")
+        zs.zero_muon_momentum(grads.cuda()[lg:], 3, n, n, dm[lm:], du[lu:], hp)
+        assert same_bits(dm[lm:], m) and same_bits(dm[:lm], mom[:lm])
+        assert same_bits(du[lu:lu + n], u.to(HF)) and not du[:lu].any() and not du[lu + n:].any()
+        lay, _ = zs.zero_flatten_layout([lg + n], 1)
+        o = torch.randn(lu + n, generator=g).to(BF)
+        full = torch.zeros(lay.n_pad, dtype=BF, device="cuda")
+        want = mom[lm:] * torch.tensor(1 - 0.02 * 0.1) - \
+            torch.tensor(0.02) * (torch.tensor(1.5) * o[lu:].float())
+        dm = mom.cuda()
+        zs.zero_muon_update(o.cuda()[lu:], dm[lm:], full, lay, 0, hp, update_scale=1.5,
+                            shard_off=lg, length=n)
+        assert same_bits(dm[lm:], want) and same_bits(full[lg:], want.to(BF))
+        assert not full[:lg].any()
+
+
 def test_momentum_controls():
     g = torch.Generator().manual_seed(1)
     n = 1003

@@ -72,6 +72,7 @@ def control(skip=None, sumsq=None, max_norm=0.0, loss_scale=None):
 
 
 LAY = zs.ZeroLayout(1000, 1000, 250, 1, 4, 0)
+HUGE3 = (ctypes.c_double * 3)(1.0, 1e300, 1.0)
 NAN3 = (ctypes.c_double * 3)(1.0, math.nan, 1.0)
 MOM = dict(grads=at(1), gdt=0, rows=4, ld=300, len=250, mom=at(2), u=at(3), udt=0, nesterov=1,
            hp=hp(), ctl=None, stream=None)
@@ -132,6 +133,9 @@ def status(op, **change):
     ("orth", dict(ns=ns(0)), EINVAL), ("orth", dict(ns=ns(33)), EINVAL),
     ("orth", dict(ns=ns(eps=-1.0)), EINVAL), ("orth", dict(ns=ns(eps=math.nan)), EINVAL),
     ("orth", dict(ns=ns(1, coeffs=ctypes.addressof(NAN3))), EINVAL),
+    ("orth", dict(ns=ns(1, coeffs=ctypes.addressof(HUGE3))), EINVAL),
+    ("orth", dict(count=65535, rows=65536, cols=65536, ldu=65536, ldo=65536, su=1 << 32,
+                  so=1 << 32, wsb=1 << 62), EINVAL),
     ("orth", dict(ws=None), EINVAL), ("orth", dict(ws=at(3, 8)), EINVAL),
     ("orth", dict(wsb=1000), EINVAL), ("orth", dict(o=at(1)), EALIAS),
     ("orth", dict(o=at(1, 2 * (2 * 64 * 70))), EALIAS), ("orth", dict(ws=at(1)), EALIAS),

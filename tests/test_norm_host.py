@@ -65,6 +65,7 @@ def status(op, **change):
     ("fwd", dict(mean=at(5, 2)), EINVAL), ("fwd", dict(rstd=at(6, 2)), EINVAL),
     ("fwd", dict(eps=0.0), EINVAL), ("fwd", dict(eps=-1.0), EINVAL),
     ("fwd", dict(eps=math.nan), EINVAL), ("fwd", dict(eps=math.inf), EINVAL),
+    ("fwd", dict(eps=1e-60), EINVAL), ("fwd", dict(eps=1e60), EINVAL),
     ("fwd", dict(ldx=1 << 60), EINVAL), ("fwd", dict(n=0), EINVAL),
     ("fwd", dict(y=at(1, 2)), EALIAS), ("fwd", dict(y=at(1), ldy=65), EALIAS),
     ("fwd", dict(y=at(1), ydt=2), EALIAS), ("fwd", dict(y=at(2)), EALIAS),

@@ -597,28 +597,34 @@ __global__ void __launch_bounds__(1024) columns_kernel(BackArgs a) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     const int64_t total = 16 * a.pieces;
-    const int64_t o = static_cast<int64_t>(blockIdx.x) * 64 + lane;
     const int each = (a.groups + 15) / 16;
-    float t = 0.0f;
-    if (o < total) {
-        const int g1 = min(a.groups, (wave + 1) * each);
+    for (int64_t o0 = static_cast<int64_t>(blockIdx.x) * 64; o0 < total;
+         o0 += static_cast<int64_t>(gridDim.x) * 64) {
+        const int64_t o = o0 + lane;
+        float t = 0.0f;
+        if (o < total) {
+            const int g1 = min(a.groups, (wave + 1) * each);
 #pragma unroll 16
-        for (int g = wave * each; g < g1; ++g) t += a.partial[g * total + o];
-    }
-    cols[wave][lane] = t;
-    __syncthreads();
-    if (wave != 0 || o >= total) return;
-    for (int v = 1; v < 16; ++v) t += cols[v][lane];
-    const int64_t e = o / a.pieces, at = (o - e * a.pieces) * 8;
-    const int64_t c = first_of(at, a.n) + (e & 7);
-    void *out = e < 8 ? a.dw : a.db;
-    if (out == nullptr || c < at || c >= a.n) return;
-    if (a.grads_f32) {
-        float *p = static_cast<float *>(out) + c;
-        *p = a.accumulate ? *p + t : t;
-    } else {
-        uint16_t *p = static_cast<uint16_t *>(out) + c;
-        *p = T::down(a.accumulate ? T::up(*p) + t : t);
+            for (int g = wave * each; g < g1; ++g) t += a.partial[g * total + o];
+        }
+        cols[wave][lane] = t;
+        __syncthreads();
+        if (wave == 0 && o < total) {
+            for (int v = 1; v < 16; ++v) t += cols[v][lane];
+            const int64_t e = o / a.pieces, at = (o - e * a.pieces) * 8;
+            const int64_t c = first_of(at, a.n) + (e & 7);
+            void *out = e < 8 ? a.dw : a.db;
+            if (out != nullptr && c >= at && c < a.n) {
+                if (a.grads_f32) {
+                    float *p = static_cast<float *>(out) + c;
+                    *p = a.accumulate ? *p + t : t;
+                } else {
+                    uint16_t *p = static_cast<uint16_t *>(out) + c;
+                    *p = T::down(a.accumulate ? T::up(*p) + t : t);
+                }
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -724,7 +730,9 @@ zero_status launch_back(BackArgs a, void *stream) {
         a.groups = 0;
     }
     if (grads)
-        columns_kernel<T><<<static_cast<uint32_t>(ceil_div(16 * a.pieces, 64)), 1024, 0, st>>>(a);
+        columns_kernel<T>
+            <<<static_cast<uint32_t>(std::min(ceil_div(16 * a.pieces, 64), kMaxGroups)), 1024, 0,
+               st>>>(a);
     return launch_status();
 }
 
@@ -752,7 +760,8 @@ zero_status zero_layernorm(const void *x, zero_dtype xdt, int64_t ldx, const voi
                            void *stream) {
     if (!is16(wdt) || !type_ok(xdt, wdt) || !type_ok(ydt, wdt) || !dim_ok(m) || !dim_ok(n))
         return ZERO_EINVAL;
-    if (!(std::isfinite(eps) && eps > 0.0)) return ZERO_EINVAL;
+    const float eps32 = static_cast<float>(eps);
+    if (!(std::isfinite(eps32) && eps32 > 0.0f)) return ZERO_EINVAL;
     const Mat mx{x, m, n, ldx, size_of(xdt)}, my{y, m, n, ldy, size_of(ydt)}, mw{w, 1, n, n, 2},
         mb{b, 1, n, n, 2}, ms{mean, 1, m, m, 4}, mr{rstd, 1, m, m, 4};
     if (!mx.ok() || !my.ok()) return ZERO_EINVAL;
@@ -767,7 +776,7 @@ zero_status zero_layernorm(const void *x, zero_dtype xdt, int64_t ldx, const voi
         overlap(sm, sr) || (overlap(sx, so) && !mx.same_place(my)))
         return ZERO_EALIAS;
     NormArgs a{x, static_cast<const uint16_t *>(w), static_cast<const uint16_t *>(b), y, mean,
-               rstd, ldx, ldy, m, n, static_cast<float>(eps)};
+               rstd, ldx, ldy, m, n, eps32, 1};
     const bool xf = xdt == ZERO_FP32, yf = ydt == ZERO_FP32;
     return wdt == ZERO_BF16 ? launch_norm<BF16>(a, xf, yf, stream)
                             : launch_norm<FP16>(a, xf, yf, stream);

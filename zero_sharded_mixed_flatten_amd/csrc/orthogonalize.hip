@@ -1239,7 +1239,7 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     if (k.steps < 1 || k.steps > ZERO_NS_MAX_STEPS || !(std::isfinite(k.eps) && k.eps >= 0.0))
         return ZERO_EINVAL;
     for (int i = 0; k.coeffs != nullptr && i < 3 * k.steps; ++i)
-        if (!std::isfinite(k.coeffs[i])) return ZERO_EINVAL;
+        if (!std::isfinite(static_cast<float>(k.coeffs[i]))) return ZERO_EINVAL;
     if (count == 0 || rows == 0 || cols == 0) return ZERO_OK;
     Span si, sr;
     if (!stack_ok(Mat{u, rows, cols, ldu, size_of(udt)}, count, su, &si) ||
