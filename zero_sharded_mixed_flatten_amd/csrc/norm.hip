@@ -463,6 +463,20 @@ __global__ void __launch_bounds__(kBackWaves *kWave) back_kernel(BackArgs a) {
         }
     }
     if constexpr (GRADS) {
+        float *sums = a.partial + static_cast<int64_t>(blockIdx.x) * 16 * a.pieces;
+        if (R == 1) {  // each column is one lane's
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int piece = (k * W + wl) * 64 + lane;
+                if (piece >= a.pieces) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sums[e * a.pieces + piece] = dw[k][e];
+                    sums[(8 + e) * a.pieces + piece] = db[k][e];
+                }
+            }
+            return;
+        }
 #pragma unroll 1
         for (int k = 0; k < K; ++k) {
             __syncthreads();
@@ -480,9 +494,8 @@ __global__ void __launch_bounds__(kBackWaves *kWave) back_kernel(BackArgs a) {
                 const int l = o & 63, e = o >> 6 & 15, v = o >> 10;
                 float t = cols[v][e][l];
                 for (int r = 1; r < R; ++r) t += cols[r * W + v][e][l];
-                const int64_t piece = static_cast<int64_t>(k * W + v) * 64 + l;
-                if (piece < a.pieces)
-                    a.partial[(static_cast<int64_t>(blockIdx.x) * 16 + e) * a.pieces + piece] = t;
+                const int piece = (k * W + v) * 64 + l;
+                if (piece < a.pieces) sums[e * a.pieces + piece] = t;
             }
         }
     }
