@@ -18,7 +18,7 @@
 //   P = E + Q:  P X = e_i X_ij + Q X
 // with X itself held to 22 bits as hi + lo in the first term, and only O, Q
 // and hi are fp16 operands.  Measured against 64 bits over flat, decaying and
-// low-rank spectra: 2^-10 of the result's norm or less.
+// low-rank spectra: 1.2e-3 of the result's norm or less.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
