@@ -99,6 +99,23 @@ def test_momentum_and_update_at_places_that_do_not_match():
         assert not full[:lg].any()
 
 
+@pytest.mark.parametrize("gt", [BF, F])
+@pytest.mark.parametrize("n_rows,n,gap", [(1, 33000, 0), (2, 32768, 1), (8, 70001, 0),
+                                          (11, 65536, 3), (64, 40003, 0), (64, 40000, 0)])
+def test_momentum_of_many_waves(gt, n_rows, n, gap):
+    """rows whose lines lie at other places than the waves'; runs and what is behind the last"""
+    g = torch.Generator().manual_seed(n)
+    for lg, lm in ((0, 0), (7, 2)):
+        grads = (torch.randn(lg + n_rows * (n + gap), generator=g) * 1e-3).to(gt)
+        mom = torch.randn(lm + n + 3, generator=g) * 1e-2
+        hp = zs.AdamWHParams(beta1=0.95, grad_scale=1.0 / n_rows)
+        m, u = momentum_cpu(grads[lg:].view(n_rows, n + gap)[:, :n], mom[lm:lm + n], hp, True)
+        dm, du = mom.cuda(), torch.zeros(n + 1, dtype=BF, device="cuda")
+        zs.zero_muon_momentum(grads.cuda()[lg:], n_rows, n + gap, n, dm[lm:lm + n], du[:n], hp)
+        assert same_bits(dm[lm:lm + n], m) and same_bits(du[:n], u.to(BF)) and not du[n:].any()
+        assert same_bits(dm[:lm], mom[:lm]) and same_bits(dm[lm + n:], mom[lm + n:])
+
+
 def test_momentum_controls():
     g = torch.Generator().manual_seed(1)
     n = 1003

@@ -45,27 +45,44 @@ __device__ __forceinline__ bool resolve(Control k, Consts &c, float &clip) {
     return true;
 }
 
-// four elements at any alignment (global memory takes it), n < 4 of them one
-// by one; fp32, or 16-bit as pairs
+// four elements at any alignment (global memory takes it); fp32, or 16-bit as
+// pairs
 typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 template <int DT>
-__device__ __forceinline__ typename GradT<DT>::quad quad_at(const typename GradT<DT>::elem *p,
-                                                            int n) {
-    if (n >= kQuad) {
-        if constexpr (DT == ZERO_FP32)
-            return __builtin_nontemporal_load(reinterpret_cast<const f32x4_any *>(p));
-        else
-            return __builtin_nontemporal_load(reinterpret_cast<const u32x2_any *>(p));
-    }
-    if constexpr (DT == ZERO_FP32) {
-        return f32x4{p[0], n > 1 ? p[1] : 0.0f, n > 2 ? p[2] : 0.0f, 0.0f};
-    } else {
-        const uint32_t b = n > 1 ? p[1] : 0u, c = n > 2 ? p[2] : 0u;
-        return u32x2{p[0] | b << 16, c};
-    }
+__device__ __forceinline__ typename GradT<DT>::quad quad_at(const typename GradT<DT>::elem *p) {
+    if constexpr (DT == ZERO_FP32)
+        return __builtin_nontemporal_load(reinterpret_cast<const f32x4_any *>(p));
+    else
+        return __builtin_nontemporal_load(reinterpret_cast<const u32x2_any *>(p));
 }
+
+// What a lane has read of a row.  A wave that holds the range's first or last
+// element may have lanes with fewer than four: all its lanes then read element
+// by element, the last one again in place of those that are not there, so that
+// these loads too go out together.  With a branch and a wait for each row the
+// one such wave set the time: 64 bf16 rows of 100003 31 us for 10.
+template <int DT, bool ENDS>
+struct Quad {
+    typename GradT<DT>::quad q;
+    __device__ __forceinline__ void read(const typename GradT<DT>::elem *p, int) {
+        q = quad_at<DT>(p);
+    }
+    __device__ __forceinline__ void widen(float (&v)[kQuad]) const { widen_quad<DT>(v, q); }
+};
+template <int DT>
+struct Quad<DT, true> {
+    typename GradT<DT>::elem e[kQuad];
+    __device__ __forceinline__ void read(const typename GradT<DT>::elem *p, int n) {
+#pragma unroll
+        for (int i = 0; i < kQuad; ++i) e[i] = p[min(i, n - 1)];
+    }
+    __device__ __forceinline__ void widen(float (&v)[kQuad]) const {
+#pragma unroll
+        for (int i = 0; i < kQuad; ++i) v[i] = widen1<DT>(e[i]);
+    }
+};
 
 template <int DT>
 __device__ __forceinline__ void quad_to(typename GradT<DT>::elem *p, const float (&v)[kQuad],
@@ -98,8 +115,19 @@ __device__ __forceinline__ void quad_to(typename GradT<DT>::elem *p, const float
 // read and written in whole cache lines but for its ends.  45 M elements from
 // element 5 on: eight bf16 rows 176 us for 236, the update 81 for 107; quads
 // aligned each by itself gain nothing.
-__device__ __forceinline__ int quad_of(int64_t len, int skew, int64_t &at) {
-    const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWave + threadIdx.x) * kQuad - skew;
+//
+// run: waves that follow one another in memory and take one XCD, 1 or kRun.
+// Workgroups go round the 8 XCDs; where the rows' lines begin at other places
+// than the waves do, two neighbours read the line between them, and runs on
+// one XCD find it in its L2.  64 fp16 rows of 479485 17.2 -> 15.6 us, eight
+// bf16 ones of 40 M + 1 180 -> 159; eight of 45 M, whole lines, 177 -> 181.
+constexpr uint32_t kXcds = 8, kRun = 16;
+
+__device__ __forceinline__ int quad_of(int64_t len, int skew, uint32_t run, int64_t &at) {
+    uint32_t block = blockIdx.x;
+    const uint32_t span = kXcds * run, in = block % span;
+    if (block - in + span <= gridDim.x) block += in % kXcds * run + in / kXcds - in;
+    const int64_t first = (static_cast<int64_t>(block) * kWave + threadIdx.x) * kQuad - skew;
     at = first < 0 ? 0 : first;
     return static_cast<int>(min(len, first + kQuad) - at);
 }
@@ -107,58 +135,96 @@ __device__ __forceinline__ int quad_of(int64_t len, int skew, int64_t &at) {
 // rows fetched together where their number is not a compile-time one
 constexpr int kBatch = 8;
 
-template <int GDT, int UDT, int NDP>
-__global__ void __launch_bounds__(kWave)
-momentum_kernel(const typename GradT<GDT>::elem *__restrict__ g, int64_t ld, int n_rows,
-                int64_t len, float *__restrict__ mom, typename GradT<UDT>::elem *__restrict__ u,
-                int nesterov, int skew, Consts c, Control ctl) {
-    float clip;
-    if (!resolve(ctl, c, clip)) return;
-    int64_t at;
-    const int n = quad_of(len, skew, at);
-    if (n <= 0) return;
-    const typename GradT<GDT>::elem *p = g + at;
+template <int GDT, int UDT>
+struct Momentum {
+    const typename GradT<GDT>::elem *__restrict__ g;
+    int64_t ld;
+    int n_rows;
+    int64_t len;
+    float *__restrict__ mom;
+    typename GradT<UDT>::elem *__restrict__ u;
+    int nesterov, skew;
+    uint32_t run;
+};
+
+template <int GDT, int UDT, int NDP, bool ENDS>
+__device__ __forceinline__ void momentum_quad(const Momentum<GDT, UDT> &w, int64_t at, int n,
+                                              const Consts &c, float clip) {
+    const typename GradT<GDT>::elem *p = w.g + at;
     constexpr int B = NDP > 0 ? NDP : kBatch;
-    typename GradT<GDT>::quad x[B];
+    Quad<GDT, ENDS> x[B];
+    Quad<ZERO_FP32, ENDS> old;
 #pragma unroll
     for (int k = 0; k < B; ++k)
-        if (NDP > 0 || k < n_rows) x[k] = quad_at<GDT>(p + k * ld, n);
-    const f32x4 old = quad_at<ZERO_FP32>(mom + at, n);
+        if (NDP > 0 || k < w.n_rows) x[k].read(p + k * w.ld, n);
+    old.read(w.mom + at, n);
     loads_issued();
     float a[kQuad], t[kQuad];
-    widen_quad<GDT>(a, x[0]);
+    x[0].widen(a);
 #pragma unroll
     for (int k = 1; k < B; ++k)
-        if (NDP > 0 || k < n_rows) {
-            widen_quad<GDT>(t, x[k]);
+        if (NDP > 0 || k < w.n_rows) {
+            x[k].widen(t);
 #pragma unroll
             for (int e = 0; e < kQuad; ++e) a[e] = a[e] + t[e];
         }
     if constexpr (NDP == 0) {
-        for (int k0 = B; k0 < n_rows; k0 += B) {
+        for (int k0 = B; k0 < w.n_rows; k0 += B) {
 #pragma unroll
             for (int k = 0; k < B; ++k)
-                if (k0 + k < n_rows) x[k] = quad_at<GDT>(p + (k0 + k) * ld, n);
+                if (k0 + k < w.n_rows) x[k].read(p + (k0 + k) * w.ld, n);
             loads_issued();
 #pragma unroll
             for (int k = 0; k < B; ++k)
-                if (k0 + k < n_rows) {
-                    widen_quad<GDT>(t, x[k]);
+                if (k0 + k < w.n_rows) {
+                    x[k].widen(t);
 #pragma unroll
                     for (int e = 0; e < kQuad; ++e) a[e] = a[e] + t[e];
                 }
         }
     }
     float m[kQuad], v[kQuad];
+    old.widen(t);
 #pragma unroll
     for (int e = 0; e < kQuad; ++e) {
         float ge = a[e] * c.s;
         if (clip < 1.0f) ge = ge * clip;
-        m[e] = c.b1 * old[e] + ge;
-        v[e] = nesterov ? ge + c.b1 * m[e] : m[e];
+        m[e] = c.b1 * t[e] + ge;
+        v[e] = w.nesterov ? ge + c.b1 * m[e] : m[e];
     }
-    quad_to<ZERO_FP32>(mom + at, m, n);
-    quad_to<UDT>(u + at, v, n);
+    quad_to<ZERO_FP32>(w.mom + at, m, n);
+    quad_to<UDT>(w.u + at, v, n);
+}
+
+template <int GDT, int UDT, int NDP>
+__global__ void __launch_bounds__(kWave)
+momentum_kernel(Momentum<GDT, UDT> w, Consts c, Control ctl) {
+    float clip;
+    if (!resolve(ctl, c, clip)) return;
+    int64_t at;
+    const int n = quad_of(w.len, w.skew, w.run, at);
+    if (n <= 0) return;
+    if (__all(n == kQuad))
+        momentum_quad<GDT, UDT, NDP, false>(w, at, n, c, clip);
+    else
+        momentum_quad<GDT, UDT, NDP, true>(w, at, n, c, clip);
+}
+
+template <int ODT, int WDT, bool ENDS>
+__device__ __forceinline__ void update_quad(const uint16_t *o, float *W, uint16_t *slot, int n,
+                                            float k, const Consts &c) {
+    Quad<ODT, ENDS> ov;
+    Quad<ZERO_FP32, ENDS> old;
+    ov.read(o, n);
+    old.read(W, n);
+    loads_issued();
+    float t[kQuad], w[kQuad];
+    ov.widen(t);
+    old.widen(w);
+#pragma unroll
+    for (int e = 0; e < kQuad; ++e) w[e] = w[e] * c.d - c.lr * (k * t[e]);
+    quad_to<ZERO_FP32>(W, w, n);
+    quad_to<WDT>(slot, w, n);
 }
 
 template <int ODT, int WDT>
@@ -168,17 +234,12 @@ update_kernel(const uint16_t *__restrict__ o, int64_t len, float *__restrict__ W
     float clip;
     if (!resolve(ctl, c, clip)) return;
     int64_t at;
-    const int n = quad_of(len, skew, at);
+    const int n = quad_of(len, skew, 1, at);
     if (n <= 0) return;
-    const u32x2 ov = quad_at<ODT>(o + at, n);
-    const f32x4 old = quad_at<ZERO_FP32>(W + at, n);
-    loads_issued();
-    float t[kQuad], w[kQuad];
-    widen_quad<ODT>(t, ov);
-#pragma unroll
-    for (int e = 0; e < kQuad; ++e) w[e] = old[e] * c.d - c.lr * (k * t[e]);
-    quad_to<ZERO_FP32>(W + at, w, n);
-    quad_to<WDT>(slot + at, w, n);
+    if (__all(n == kQuad))
+        update_quad<ODT, WDT, false>(o + at, W + at, slot + at, n, k, c);
+    else
+        update_quad<ODT, WDT, true>(o + at, W + at, slot + at, n, k, c);
 }
 
 // ---------------------------------------------------------------------------
@@ -217,9 +278,13 @@ void run_momentum(const void *grads, int64_t ld, int32_t n_rows, int64_t len, fl
     const int waves = GDT == ZERO_FP32 ? (n_rows >= 8 ? 8 : 16)
                                        : (n_rows >= 8 ? 12 : n_rows == 1 ? 16 : 20);
     const size_t lds = residency(waves, len);
+    constexpr int64_t kSize = sizeof(*g), kLine = 128;
+    const int64_t off = reinterpret_cast<intptr_t>(g) - reinterpret_cast<intptr_t>(mom) / 4 * kSize;
+    const uint32_t run = off % kLine != 0 || (n_rows > 1 && ld % (kLine / kSize) != 0) ? kRun : 1;
     for_launches(len, [&](int64_t at, int64_t n) {
         momentum_kernel<GDT, UDT, NDP><<<groups_of(n, skew_of(mom)), kWave, lds, st>>>(
-            g + at, ld, n_rows, n, mom + at, out + at, nesterov != 0, skew_of(mom), c, k);
+            Momentum<GDT, UDT>{g + at, ld, n_rows, n, mom + at, out + at, nesterov != 0,
+                               skew_of(mom), run}, c, k);
     });
 }
 
