@@ -219,6 +219,29 @@ def test_backward_over_types(t, xf, yf, gf, residual):
         check_backward(dy, x, w, mean, rstd, res, dx, dw, db)
 
 
+@pytest.mark.parametrize("n", [513, 2200, 3584, 3700, 4104, 5555, 8185, 8192, 8193, 12300])
+@pytest.mark.parametrize("xt,yt", [(BF, BF), (F, F), (BF, F)])
+def test_backward_of_each_split(n, xt, yt):
+    """rows of 2 to 16 waves and of more than a piece a lane, some of them idle at the end"""
+    for m in (300, 2100):
+        dy, x, w, mean, rstd, res, dx, dxbuf, dw, db, row = \
+            backward_case(gen(n + m), m, n, BF, xt, yt, F, m == 300)
+        zs.zero_layernorm_backward(dy, x, w, mean, rstd, dx, residual=res, dw=dw, db=db)
+        check_backward(dy, x, w, mean, rstd, res, dx, dw, db)
+
+
+@pytest.mark.parametrize("n", [513, 2200, 4097, 5000, 7000, 8192, 11000])
+@pytest.mark.parametrize("xf,yf", [(True, True), (True, False), (False, True)])
+def test_forward_of_each_split(n, xf, yf):
+    g = gen(n)
+    for m in (513, 4099):
+        x, _ = rows(g, m, n, 1, F if xf else BF, off=1, shift=0.5)
+        w, b = (torch.randn(n, generator=g, device="cuda").to(BF) for _ in range(2))
+        y, _ = rows(g, m, n, 0, F if yf else BF, off=1)
+        zs.zero_layernorm(x, w, b, y, eps=EPS)
+        check_forward(x, w, b, y, None, None)
+
+
 @pytest.mark.parametrize("n", [100, 1600, 20000])
 def test_backward_without_some_gradients(n):
     dy, x, _, mean, rstd, res, dx, _, dw, db, row = \

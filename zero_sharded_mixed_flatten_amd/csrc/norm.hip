@@ -361,16 +361,19 @@ struct BackArgs {
 };
 
 constexpr int kBackWaves = 8;
-constexpr int kGroups = 512;        // workgroups that keep column sums
+constexpr int kRowWaves = 16;  // of a row, one piece a lane
+constexpr int kGroups = 512;   // workgroups that keep column sums
 
-// A workgroup of eight waves takes rows in turn, R = 8 / W of them at a time.
+// A workgroup takes rows in turn, R at a time: as many as eight waves hold, or
+// one of more waves.
 // A lane has the same columns of all of them, so the sums of dw and db stay
 // in its registers until the end, where they are joined over the rows in
 // shared memory and stored once a workgroup.  The next rows are loaded before
 // the current ones' sums are joined (PF, where the registers hold both).
 template <class T, bool XF, bool DF, int K, bool GRADS, bool PF>
-__global__ void __launch_bounds__(kBackWaves *kWave) back_kernel(BackArgs a) {
-    __shared__ float part[2][kBackWaves][2];
+__global__ void __launch_bounds__((K == 1 ? kRowWaves : kBackWaves) * kWave)
+back_kernel(BackArgs a) {
+    __shared__ float part[2][K == 1 ? kRowWaves : kBackWaves][2];
     __shared__ float cols[GRADS ? kBackWaves : 1][16][kWave];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
@@ -646,12 +649,15 @@ __global__ void __launch_bounds__(1024) columns_kernel(BackArgs a) {
 
 constexpr int64_t kMaxGroups = int64_t(1) << 21;  // a launch has less than 2^32 threads
 
-
 template <class T, bool XF, bool YF, int K>
 void run_norm(const NormArgs &a, hipStream_t st) {
-    // as many workgroups as stay on the card at once, for their registers
-    const int W = a.waves_a_row, R = std::max(1, 4 / W);
-    const int a_cu = std::max(1, (K == 4 ? 12 : 16) / (W * R));
+    // As many workgroups as stay on the card at once, for their registers;
+    // from fp32 to fp32, twice the bytes under way, fewer waves in larger
+    // workgroups with two pieces a lane keep HBM busiest (16384 x 4096
+    // 102 -> 95 us; to 16-bit 74 -> 72, but rows of 3500 67 -> 76).
+    constexpr bool kBulk = XF && YF && K > 1;
+    const int W = a.waves_a_row, R = std::max(1, (kBulk ? 8 : 4) / W);
+    const int a_cu = std::max(1, (kBulk || K == 4 ? 12 : 16) / (W * R));
     const uint32_t g =
         static_cast<uint32_t>(std::min<int64_t>(ceil_div(a.m, R), kCUs * a_cu));
     if (W > 1)
@@ -680,9 +686,10 @@ zero_status launch_norm(NormArgs a, void *stream) {
         return launch_status();
     }
     const int64_t waves = ceil_div(a.n, 512);  // of one piece a lane
-    // Few rows are spread over waves.  Otherwise four pieces a lane, three
-    // beyond 8192 elements, where eight waves are enough for those.
-    const int pieces = a.m <= 512 ? 1 : waves <= 16 ? 4 : 3;
+    // Few rows are spread over waves.  Otherwise four pieces a lane (fp32 to
+    // fp32 two), three beyond 8192 elements, where eight waves are enough for
+    // those.
+    const int pieces = a.m <= 512 ? 1 : waves > 16 ? 3 : XF && YF ? 2 : 4;
     a.waves_a_row = static_cast<int32_t>(std::min<int64_t>(8, ceil_div(waves, pieces)));
     switch (ceil_div(waves, a.waves_a_row)) {
         case 1: run_norm<T, XF, YF, 1>(a, st); break;
@@ -701,7 +708,7 @@ zero_status launch_norm(const NormArgs &a, bool xf, bool yf, void *stream) {
 
 template <class T, bool XF, bool DF, int K>
 void run_back(const BackArgs &a, int threads, bool grads, hipStream_t st) {
-    constexpr bool PF = K <= (XF || DF ? 2 : 3);  // what the registers hold
+    constexpr bool PF = K <= (XF || DF ? 1 : 3);  // what the registers hold
     if (grads)
         back_kernel<T, XF, DF, K, true, PF><<<a.groups, threads, 0, st>>>(a);
     else
@@ -714,19 +721,22 @@ zero_status launch_back(BackArgs a, void *stream) {
     const bool grads = a.dw != nullptr || a.db != nullptr;
     const int64_t waves = ceil_div(a.n, 512);
     if (a.m > 0 && in_registers(a.n)) {
-        // One piece a lane up to 2048 elements, with two workgroups on a CU;
-        // beyond, two (three from 8192 on), with one, which keeps the column
-        // sums that go through memory few.
-        const int W = static_cast<int>(
-            std::min<int64_t>(kBackWaves, ceil_div(waves, waves <= 4 ? 1 : 2)));
-        const int R = kBackWaves / W;
+        // One piece a lane up to 8192 elements, three or four beyond.  One
+        // workgroup on a CU keeps the column sums that go through memory few;
+        // two of them pay for 16-bit rows where those of one are less than
+        // eight waves' and each has rows enough (4096 x 2304 30.4 -> 25.7 us,
+        // 4096 x 4096 35.9 -> 37.3, 1023 x 2304 15.0 -> 15.3; fp32 3008 wide
+        // 43.7 -> 46.9).
+        const int W = static_cast<int>(std::min<int64_t>(waves <= kRowWaves ? kRowWaves : kBackWaves,
+                                                         waves));
+        const int R = std::max(1, kBackWaves / W);
         a.waves_a_row = W;
-        a.groups = static_cast<int32_t>(
-            std::min<int64_t>(waves <= 4 ? kGroups : kGroups / 2, ceil_div(a.m, R)));
+        const int64_t turns = ceil_div(a.m, R);
+        a.groups = static_cast<int32_t>(std::min<int64_t>(
+            !XF && !DF && W < kBackWaves && turns >= 4 * kGroups ? kGroups : kGroups / 2, turns));
         const int threads = W * R * kWave;
         switch (ceil_div(waves, W)) {
             case 1: run_back<T, XF, DF, 1>(a, threads, grads, st); break;
-            case 2: run_back<T, XF, DF, 2>(a, threads, grads, st); break;
             case 3: run_back<T, XF, DF, 3>(a, threads, grads, st); break;
             default: run_back<T, XF, DF, 4>(a, threads, grads, st); break;
         }
