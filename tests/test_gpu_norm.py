@@ -230,6 +230,27 @@ def test_backward_of_each_split(n, xt, yt):
         check_backward(dy, x, w, mean, rstd, res, dx, dw, db)
 
 
+@pytest.mark.parametrize("m", [1, 7, 64, 511, 512, 513])
+@pytest.mark.parametrize("n", [8, 129, 1601, 5000, 9001, 16384])
+@pytest.mark.parametrize("gt", [BF, F])
+def test_backward_of_few_rows(m, n, gt):
+    """dx and the column sums by different workgroups; in place by one kind after the other"""
+    dy, x, w, mean, rstd, res, dx, dxbuf, dw, db, row = \
+        backward_case(gen(n + m), m, n, BF, BF, BF, gt, True)
+    canaries = row[0].item(), row[n + 1].item(), row[-1].item()
+    zs.zero_layernorm_backward(dy, x, w, mean, rstd, dx, residual=res, dw=dw, db=db)
+    check_backward(dy, x, w, mean, rstd, res, dx, dw, db)
+    first = dw.clone(), db.clone()
+    zs.zero_layernorm_backward(dy, x, w, mean, rstd, dx, residual=res, dw=dw, accumulate=True)
+    assert torch.equal(db, first[1])
+    zs.zero_layernorm_backward(dy, x, w, mean, rstd, dx, residual=res, db=db, accumulate=True)
+    check_backward(dy, x, w, mean, rstd, res, dx, dw, db, old=first)
+    assert canaries == (row[0].item(), row[n + 1].item(), row[-1].item())
+    kept = dy.clone()
+    zs.zero_layernorm_backward(dy, x, w, mean, rstd, dy, residual=dy, dw=dw, db=db)
+    check_backward(kept, x, w, mean, rstd, kept, dy, dw, db)
+
+
 @pytest.mark.parametrize("n", [513, 2200, 4097, 5000, 7000, 8192, 11000])
 @pytest.mark.parametrize("xf,yf", [(True, True), (True, False), (False, True)])
 def test_forward_of_each_split(n, xf, yf):

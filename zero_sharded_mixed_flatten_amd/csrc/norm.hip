@@ -363,16 +363,90 @@ struct BackArgs {
 constexpr int kBackWaves = 8;
 constexpr int kRowWaves = 16;  // of a row, one piece a lane
 constexpr int kGroups = 512;   // workgroups that keep column sums
+constexpr int kFewRows = 512;  // whose column sums are other workgroups'
+
+// where a piece's eight columns start
+__device__ __forceinline__ int64_t first_of(int64_t at, int64_t n) {
+    return n >= 8 ? min(at, n - 8) : 0;
+}
+
+// a column's sum over all rows, t, to its place: value e (dw 0..7, db 8..15)
+// of a piece
+template <class T>
+__device__ __forceinline__ void put_column(const BackArgs &a, int e, int64_t piece, float t) {
+    const int64_t at = piece * 8, c = first_of(at, a.n) + (e & 7);
+    void *out = e < 8 ? a.dw : a.db;
+    if (out == nullptr || c < at || c >= a.n) return;
+    if (a.grads_f32) {
+        float *p = static_cast<float *>(out) + c;
+        *p = a.accumulate ? *p + t : t;
+    } else {
+        uint16_t *p = static_cast<uint16_t *>(out) + c;
+        *p = T::down(a.accumulate ? T::up(*p) + t : t);
+    }
+}
+
+// The column sums of few rows, by workgroups behind those of dx: dw and db
+// need mean and rstd only, not the rows' sums.  A workgroup has the columns of
+// 16 pieces, 16 lanes of it take every so manyth row.
+constexpr int kFewPieces = 16;
+
+template <class T, bool XF, bool DF, int WAVES>
+__device__ __forceinline__ void few_columns(const BackArgs &a, int64_t block) {
+    __shared__ float sums[WAVES * kWave / kFewPieces][16][kFewPieces];
+    const int at_once = static_cast<int>(blockDim.x) / kFewPieces;
+    const int l = threadIdx.x % kFewPieces, mine = threadIdx.x / kFewPieces;
+    const int64_t c = first_of(min(block * kFewPieces + l, a.pieces - 1) * 8, a.n);
+    float dw[8], db[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[e] = db[e] = 0.0f;
+#pragma unroll 4
+    for (int64_t row = mine; row < a.m; row += at_once) {
+        Oct<T, XF> x;
+        Oct<T, DF> dy;
+        x.whole(a.x, row * a.ldx + c);
+        dy.whole(a.dy, row * a.lddy + c);
+        const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            dw[e] = __builtin_fmaf(dy.at(e), (x.at(e) - mean) * rstd, dw[e]);
+            db[e] += dy.at(e);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        sums[mine][e][l] = dw[e];
+        sums[mine][8 + e][l] = db[e];
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < 16 * kFewPieces; o += static_cast<int>(blockDim.x)) {
+        const int e = o / kFewPieces, v = o % kFewPieces;
+        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r = 0; r < at_once; r += 4)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] += sums[r + k][e][v];
+        const int64_t piece = block * kFewPieces + v;
+        if (piece < a.pieces) put_column<T>(a, e, piece, (t[0] + t[1]) + (t[2] + t[3]));
+    }
+}
 
 // A workgroup takes rows in turn, R at a time: as many as eight waves hold, or
 // one of more waves.
 // A lane has the same columns of all of them, so the sums of dw and db stay
 // in its registers until the end, where they are joined over the rows in
 // shared memory and stored once a workgroup.  The next rows are loaded before
-// the current ones' sums are joined (PF, where the registers hold both).
-template <class T, bool XF, bool DF, int K, bool GRADS, bool PF>
+// the current ones' sums are joined (PF, where the registers hold both).  Of
+// few rows (FEW) the sums are other workgroups' of the launch.
+enum Grads { NONE, SUMS, FEW };
+
+template <class T, bool XF, bool DF, int K, Grads HOW, bool PF>
 __global__ void __launch_bounds__((K == 1 ? kRowWaves : kBackWaves) * kWave)
 back_kernel(BackArgs a) {
+    constexpr bool GRADS = HOW == SUMS;
+    if constexpr (HOW == FEW) {
+        if (blockIdx.x >= static_cast<uint32_t>(a.groups))
+            return few_columns<T, XF, DF, K == 1 ? kRowWaves : kBackWaves>(a, blockIdx.x - a.groups);
+    }
     __shared__ float part[2][K == 1 ? kRowWaves : kBackWaves][2];
     __shared__ float cols[GRADS ? kBackWaves : 1][16][kWave];
     const int lane = threadIdx.x & 63;
@@ -380,7 +454,7 @@ back_kernel(BackArgs a) {
     const int W = a.waves_a_row, R = (static_cast<int>(blockDim.x) >> 6) / W;
     const int rg = wave / W, wl = wave - rg * W;
     const float n = static_cast<float>(a.n);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+    const int64_t step = static_cast<int64_t>(a.groups) * R;
     struct Row {
         Oct<T, XF> x[K], r[K];
         Oct<T, DF> dy[K];
@@ -558,11 +632,6 @@ __global__ void __launch_bounds__(1024) back_loop_kernel(BackArgs a) {
     }
 }
 
-// where a piece's eight columns start
-__device__ __forceinline__ int64_t first_of(int64_t at, int64_t n) {
-    return n >= 8 ? min(at, n - 8) : 0;
-}
-
 // the column sums of such rows, before dx may be written over dy: a lane has
 // a piece, the eight waves of a workgroup and the workgroups along y take
 // rows in turn
@@ -627,18 +696,8 @@ __global__ void __launch_bounds__(1024) columns_kernel(BackArgs a) {
         __syncthreads();
         if (wave == 0 && o < total) {
             for (int v = 1; v < 16; ++v) t += cols[v][lane];
-            const int64_t e = o / a.pieces, at = (o - e * a.pieces) * 8;
-            const int64_t c = first_of(at, a.n) + (e & 7);
-            void *out = e < 8 ? a.dw : a.db;
-            if (out != nullptr && c >= at && c < a.n) {
-                if (a.grads_f32) {
-                    float *p = static_cast<float *>(out) + c;
-                    *p = a.accumulate ? *p + t : t;
-                } else {
-                    uint16_t *p = static_cast<uint16_t *>(out) + c;
-                    *p = T::down(a.accumulate ? T::up(*p) + t : t);
-                }
-            }
+            const int64_t e = o / a.pieces;
+            put_column<T>(a, static_cast<int>(e), o - e * a.pieces, t);
         }
         __syncthreads();
     }
@@ -707,12 +766,16 @@ zero_status launch_norm(const NormArgs &a, bool xf, bool yf, void *stream) {
 }
 
 template <class T, bool XF, bool DF, int K>
-void run_back(const BackArgs &a, int threads, bool grads, hipStream_t st) {
+void run_back(const BackArgs &a, int threads, Grads how, hipStream_t st) {
     constexpr bool PF = K <= (XF || DF ? 1 : 3);  // what the registers hold
-    if (grads)
-        back_kernel<T, XF, DF, K, true, PF><<<a.groups, threads, 0, st>>>(a);
-    else
-        back_kernel<T, XF, DF, K, false, false><<<a.groups, threads, 0, st>>>(a);
+    if (how == SUMS) {
+        back_kernel<T, XF, DF, K, SUMS, PF><<<a.groups, threads, 0, st>>>(a);
+    } else if (how == FEW) {
+        const uint32_t g = a.groups + static_cast<uint32_t>(ceil_div(a.pieces, kFewPieces));
+        back_kernel<T, XF, DF, K, FEW, false><<<g, threads, 0, st>>>(a);
+    } else {
+        back_kernel<T, XF, DF, K, NONE, false><<<a.groups, threads, 0, st>>>(a);
+    }
 }
 
 template <class T, bool XF, bool DF>
@@ -720,6 +783,7 @@ zero_status launch_back(BackArgs a, void *stream) {
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const bool grads = a.dw != nullptr || a.db != nullptr;
     const int64_t waves = ceil_div(a.n, 512);
+    Grads how = grads ? SUMS : NONE;
     if (a.m > 0 && in_registers(a.n)) {
         // One piece a lane up to 8192 elements, three or four beyond.  One
         // workgroup on a CU keeps the column sums that go through memory few;
@@ -735,10 +799,16 @@ zero_status launch_back(BackArgs a, void *stream) {
         a.groups = static_cast<int32_t>(std::min<int64_t>(
             !XF && !DF && W < kBackWaves && turns >= 4 * kGroups ? kGroups : kGroups / 2, turns));
         const int threads = W * R * kWave;
+        // One launch for two, which read x and dy twice: a row of 1600 7.3 ->
+        // 3.0 us, 256 rows 10.7 -> 4.7, 512 10.7 -> 10.1, 1023 11.7 -> 17.8;
+        // 256 of 11008 18.9 -> 9.6, 512 of 600 9.7 -> 6.5 (replayed from a
+        // graph).  Not in place: nobody may write dy before the columns'
+        // workgroups have read it.
+        if (grads && a.m <= kFewRows && a.dx != a.dy) how = FEW;
         switch (ceil_div(waves, W)) {
-            case 1: run_back<T, XF, DF, 1>(a, threads, grads, st); break;
-            case 3: run_back<T, XF, DF, 3>(a, threads, grads, st); break;
-            default: run_back<T, XF, DF, 4>(a, threads, grads, st); break;
+            case 1: run_back<T, XF, DF, 1>(a, threads, how, st); break;
+            case 3: run_back<T, XF, DF, 3>(a, threads, how, st); break;
+            default: run_back<T, XF, DF, 4>(a, threads, how, st); break;
         }
     } else if (a.m > 0) {
         a.groups = static_cast<int32_t>(std::min<int64_t>(16, ceil_div(a.m, kBackWaves)));
@@ -752,7 +822,7 @@ zero_status launch_back(BackArgs a, void *stream) {
     } else {
         a.groups = 0;
     }
-    if (grads)
+    if (how == SUMS)
         columns_kernel<T>
             <<<static_cast<uint32_t>(std::min(ceil_div(16 * a.pieces, 64), kMaxGroups)), 1024, 0,
                st>>>(a);
