@@ -379,3 +379,20 @@ def test_orthogonalize_large(count, r, c):
     zs.zero_orthogonalize(u, o)
     for i in range(count):
         check_orth(o[i], ns64(u[i]), f"matrix {i}")
+
+
+@pytest.mark.parametrize("r,c", [(1, 8), (9, 17), (33, 1023), (64, 1024), (1024, 63), (64, 1025),
+                                 (65, 448), (127, 447), (448, 128), (100, 385), (128, 449),
+                                 (449, 70)])
+@pytest.mark.parametrize("ut", [BF, HF, F])
+def test_orthogonalize_up_to_one_workgroups_sizes(r, c, ut):
+    """the last sizes that shared memory holds and the first that it does not; rows' odd ends"""
+    g = gen(r + c)
+    for ot, tall_ld in ((BF, c + 1), (HF, c)):
+        u = torch.randn(2, r, tall_ld, generator=g, device="cuda").to(ut)[:, :, :c]
+        buf = torch.full((2, r, tall_ld + 2), 7.0, dtype=ot, device="cuda")
+        o = buf[:, :, 1:c + 1]
+        zs.zero_orthogonalize(u, o)
+        for k in range(2):
+            check_orth(o[k], ns64(u[k]), f"{r} x {c}")
+        assert (buf[:, :, 0] == 7).all() and (buf[:, :, c + 1:] == 7).all()

@@ -84,6 +84,29 @@ __device__ __forceinline__ void eight(const void *p, int64_t at, int n, float (&
     }
 }
 
+// eight elements as they lie in memory, to have the loads of several under way
+template <int DT>
+struct Raw {
+    u16x8 h;
+    __device__ __forceinline__ void clear() { h = u16x8{}; }
+    __device__ __forceinline__ void load(const void *p, int64_t at) {
+        __builtin_memcpy(&h, static_cast<const uint16_t *>(p) + at, 16);
+    }
+    __device__ __forceinline__ float at(int e) const {
+        return DT == ZERO_BF16 ? BF16::up(h[e]) : FP16::up(h[e]);
+    }
+};
+template <>
+struct Raw<ZERO_FP32> {
+    f32x4 a, b;
+    __device__ __forceinline__ void clear() { a = b = f32x4{0.f, 0.f, 0.f, 0.f}; }
+    __device__ __forceinline__ void load(const void *p, int64_t at) {
+        __builtin_memcpy(&a, static_cast<const float *>(p) + at, 16);
+        __builtin_memcpy(&b, static_cast<const float *>(p) + at + 4, 16);
+    }
+    __device__ __forceinline__ float at(int e) const { return e < 4 ? a[e & 3] : b[e & 3]; }
+};
+
 // ---------------------------------------------------------------------------
 // |U|^2 in up to kParts fp64 parts a matrix: pieces of eight elements, in turn
 
@@ -145,16 +168,19 @@ __device__ __forceinline__ u32x4 pack(const float (&v)[8]) {
             uint32_t, __builtin_convertvector(f32x2{v[2 * p], v[2 * p + 1]}, f16x2));
     return h;
 }
+// hi and what it leaves of v, in one instruction an element: a subtraction and
+// the rounding of its exact result, which needs the factor kept from sight
 __device__ __forceinline__ void split8(const float (&v)[8], u32x4 &hi, u32x4 &lo) {
     hi = pack(v);
-    float rest[8];
+    float minus = -1.0f;
+    asm("" : "+s"(minus));
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const f32x2 h = pair(hi, p);
-        rest[2 * p] = v[2 * p] - h[0];
-        rest[2 * p + 1] = v[2 * p + 1] - h[1];
+        lo[p] = __builtin_bit_cast(
+            uint32_t, f16x2{static_cast<_Float16>(__builtin_fmaf(h[0], minus, v[2 * p])),
+                            static_cast<_Float16>(__builtin_fmaf(h[1], minus, v[2 * p + 1]))});
     }
-    lo = pack(rest);
 }
 
 // kScale / (sqrt(s) + eps); NaN where a matrix has an Inf or a NaN, which is
@@ -640,11 +666,12 @@ __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kerne
 // Small matrices: one workgroup does all rounds of a matrix, with X (hi), A
 // and P in shared memory; only lo goes through the workspace.  The products'
 // launches, seventeen for five rounds, take at least 4 us each.  A call by one
-// workgroup a matrix : by launches, us: 64 x 64 15 : 60, 64 x 512 39 : 73,
-// 64 x 1024 69 : 84 (its transpose 91 : 85), 128 x 128 44 : 70, 128 x 320
-// 71 : 75, 48 of 64 x 1024 72 : 125, 1000 of 64 x 64 62 : 596.  A CU's vector
-// units (hi and lo of every element, each round) and its reads of shared
-// memory bound it; longer rows are left to the products, which have all CUs.
+// workgroup a matrix : by launches, us: 64 x 64 14 : 60, 64 x 512 32 : 73,
+// 64 x 1024 56 : 84 (its transpose 62 : 85), 128 x 128 34 : 70, 128 x 384
+// 61 : 71, 128 x 448 71 : 74, 48 of 64 x 1024 58 : 125, 300 of 128 x 448
+// 152 : 357, 1000 of 64 x 64 53 : 596.  A CU's vector units (hi and lo of every
+// element, each round) and its reads of shared memory bound it; longer rows,
+// which shared memory does not hold, are left to the products.
 //
 // X and A lie row by row in 16-byte pieces, piece s of row i at s ^ tw(i): tw
 // differs for any eight rows in turn, and among four of them in the units of
@@ -778,7 +805,19 @@ struct SmallArgs {
 };
 
 template <int R>
-constexpr int kSmallColumns = R == 64 ? 1024 : 320;  // of the longest rows
+constexpr int kSmallColumns = R == 64 ? 1024 : 448;  // of the longest rows
+
+// Where row i's eight lo from column j on lie.  Of 64 rows as the waves have
+// them when they make X = P X, lane by lane, 16 rows of 32 columns at a time:
+// row by row, 16 rows of 1024 fell on two channels of the L2 (13.8 -> 10.3
+// thousand cycles a round).  Of 128 shorter rows row by row (11.3; 12.3).
+template <int R>
+__device__ __forceinline__ int lo_of(int i, int j, int C) {
+    return R == 64 ? ((j / 32 * (R / 16) + i / 16) * kWave + j / 8 % 4 * 16 + i % 16) * 8
+                   : i * C + j;
+}
+
+constexpr int kAhead = 4;  // pieces a lane has under way
 
 template <int DT, int R>
 __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) {
@@ -794,19 +833,31 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
     const int r = a.tall ? a.in.cols : a.in.rows, c = a.tall ? a.in.rows : a.in.cols;
     uint16_t *lo = a.lo + m * R * C;
 
-    // |U|^2
+    // |U|^2: whole pieces, kAhead of them under way, then the rows' ends
     double s = 0.0;
     {
-        const int a_row = (a.in.cols + 7) / 8, total = a_row * a.in.rows;
-        for (int p = tid; p < total; p += THREADS) {
-            const int i = p / a_row, j = (p - i * a_row) * 8;
-            float v[8];
-            eight<DT>(a.in.u, base + i * a.in.ldu + j, a.in.cols - j, v);
+        const int a_row = a.in.cols / 8, total = a_row * a.in.rows, rest = a.in.cols % 8;
+        for (int p0 = tid; p0 < total; p0 += kAhead * THREADS) {
+            Raw<DT> u[kAhead];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const double d = static_cast<double>(v[e]);
-                s = __builtin_fma(d, d, s);
+            for (int b = 0; b < kAhead; ++b) {
+                const int p = p0 + b * THREADS, i = p / a_row;
+                u[b].clear();
+                if (p < total) u[b].load(a.in.u, base + i * a.in.ldu + (p - i * a_row) * 8);
             }
+#pragma unroll
+            for (int b = 0; b < kAhead; ++b)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const double d = static_cast<double>(u[b].at(e));
+                    s = __builtin_fma(d, d, s);
+                }
+        }
+        for (int p = tid; p < rest * a.in.rows; p += THREADS) {
+            const int i = p / rest;
+            const double d = static_cast<double>(
+                element<DT>(a.in.u, base + i * a.in.ldu + a_row * 8 + p - i * rest));
+            s = __builtin_fma(d, d, s);
         }
     }
     s = wave_sum(s);
@@ -816,49 +867,81 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
 #pragma unroll
     for (int w = 0; w < kSmallWaves; ++w) s += wave_part[w];
     const double inv = scale_of(s, a.eps);
-    // X; neighbouring lanes take neighbouring pieces of a row, or (tall) of a
-    // column, whichever are neighbours in memory
-    const int a_row = C / 8;
-    for (int p = tid; p < R * a_row; p += THREADS) {
-        const int i = a.tall ? p % R : p / a_row, j = (a.tall ? p / R : p % a_row) * 8;
-        float v[8];
-        if (a.tall) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = i < r && j + e < c ? element<DT>(a.in.u, base + (j + e) * a.in.ldu + i)
-                                          : 0.0f;
-        } else {
-            eight<DT>(a.in.u, base + i * a.in.ldu + j, i < r ? c - j : 0, v);
-        }
+    // X
+    const auto set = [&](int i, int j, float (&v)[8]) __attribute__((always_inline)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            v[e] = i < r && j + e < c ? static_cast<float>(static_cast<double>(v[e]) * inv) : 0.0f;
+            v[e] = static_cast<float>(static_cast<double>(v[e]) * inv);
         u32x4 h, l;
         split8(v, h, l);
         *reinterpret_cast<u32x4 *>(X + piece_of(i, C, j / 8)) = h;
-        *reinterpret_cast<u32x4 *>(lo + i * C + j) = l;
+        *reinterpret_cast<u32x4 *>(lo + lo_of<R>(i, j, C)) = l;
+    };
+    const int a_row = C / 8;
+    if (a.tall) {  // a column's elements; neighbouring lanes have neighbouring columns
+        constexpr int B = kAhead / 2;
+        for (int p0 = tid; p0 < R * a_row; p0 += B * THREADS) {
+            float v[B][8];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int p = min(p0 + b * THREADS, R * a_row - 1);
+                const int64_t at = base + min(p % R, r - 1);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[b][e] = element<DT>(a.in.u, at + min(p / R * 8 + e, c - 1) * a.in.ldu);
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int p = p0 + b * THREADS, i = p % R, j = p / R * 8;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[b][e] = i < r && j + e < c ? v[b][e] : 0.0f;
+                if (p < R * a_row) set(i, j, v[b]);
+            }
+        }
+    } else {
+        for (int p0 = tid; p0 < R * a_row; p0 += kAhead * THREADS) {
+            Raw<DT> u[kAhead];
+#pragma unroll
+            for (int b = 0; b < kAhead; ++b) {
+                const int p = p0 + b * THREADS, i = p / a_row, j = (p - i * a_row) * 8;
+                u[b].clear();
+                if (i < r && j + 8 <= c) u[b].load(a.in.u, base + i * a.in.ldu + j);
+            }
+#pragma unroll
+            for (int b = 0; b < kAhead; ++b) {
+                const int p = p0 + b * THREADS, i = p / a_row, j = (p - i * a_row) * 8;
+                if (i >= R || (i < r && j < c && j + 8 > c)) continue;
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = u[b].at(e);
+                set(i, j, v);
+            }
+        }
+        if (c % 8 != 0 && tid < r) {  // the rows' ends
+            const int j = c & ~7;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = element<DT>(a.in.u, base + tid * a.in.ldu + min(j + e, c - 1));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = j + e < c ? v[e] : 0.0f;
+            set(tid, j, v);
+        }
     }
     __syncthreads();
 
-    Square<R> square(wave, lane);
-#pragma unroll 1
-    for (int step = 0; step < a.steps; ++step) {
-        square.clear();
-#pragma unroll 1
-        for (int k = 0; k < C; k += 64) square.multiply(X, C, k);
-        square.put(A, diag);
-        __syncthreads();
-        square.polynomial(A, diag, a.coeffs[3 * step], a.coeffs[3 * step + 1],
-                          a.coeffs[3 * step + 2]);
-        // X = P X: a wave has all rows of 32 columns at a time, and is the only
-        // one to read and to write them
+    // X = P X: a wave has all rows of 32 columns at a time, and is the only
+    // one to read and to write them.  The last time it is the result; a copy of
+    // the code of its own, or its conversions are made every time.
+    uint16_t *const out = static_cast<uint16_t *>(a.o) + m * a.so;
+    const auto apply = [&](auto last) __attribute__((always_inline)) {
 #pragma unroll 1
         for (int j0 = wave * 32; j0 < C; j0 += kSmallWaves * 32) {
             const int j = j0 + g * 8;
             u32x4 l[R / 16];
 #pragma unroll
             for (int f = 0; f < R / 16; ++f)
-                l[f] = *reinterpret_cast<const u32x4 *>(lo + (f * 16 + (lane & 15)) * C + j);
+                l[f] = *reinterpret_cast<const u32x4 *>(lo + lo_of<R>(f * 16 + (lane & 15), j, C));
             __builtin_amdgcn_sched_barrier(0);
             f32x4 x[R / 16][2];
 #pragma unroll
@@ -882,48 +965,80 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
 #pragma unroll
                         for (int b = 0; b < 2; ++b) x[f][b] = mfma<FP16>(q[h][b], p[h][f], x[f][b]);
             }
+            constexpr int G = R == 64 ? 4 : 1;  // rows of hi read ahead, as registers allow
+            u32x4 xh[G];
+            float d[G];
 #pragma unroll
             for (int f = 0; f < R / 16; ++f) {
-                __builtin_amdgcn_sched_barrier(0);
                 const int i = f * 16 + (lane & 15);
+                if (f % G == 0) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int q = 0; q < G; ++q) {
+                        xh[q] = *reinterpret_cast<const u32x4 *>(
+                            X + piece_of(i + 16 * q, C, j / 8));
+                        d[q] = diag[i + 16 * q];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
                 uint16_t *xp = X + piece_of(i, C, j / 8);
-                const u32x4 h = *reinterpret_cast<const u32x4 *>(xp);
-                const float e_i = diag[i];
+                const u32x4 h = xh[f % G];
+                const float e_i = d[f % G];
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] = __builtin_fmaf(
-                        e_i, pair(h, e / 2)[e & 1] + pair(l[f], e / 2)[e & 1],
-                        x[f][e / 4][e & 3] * kInv);
-                if (step + 1 < a.steps) {
+                    v[e] = __builtin_fmaf(pair(h, e / 2)[e & 1], e_i,
+                                          __builtin_fmaf(pair(l[f], e / 2)[e & 1], e_i,
+                                                         x[f][e / 4][e & 3] * kInv));
+                if constexpr (!decltype(last)::value) {
                     u32x4 nh, nl;
                     split8(v, nh, nl);
                     *reinterpret_cast<u32x4 *>(xp) = nh;
-                    *reinterpret_cast<u32x4 *>(lo + i * C + j) = nl;
+                    *reinterpret_cast<u32x4 *>(lo + lo_of<R>(i, j, C)) = nl;
                 } else if (i < r) {
-                    uint16_t *o = static_cast<uint16_t *>(a.o) + m * a.so;
-                    u16x8 y;
+                    u32x4 y;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] = a.bf16 ? BF16::down(v[e] * kInv) : FP16::down(v[e] * kInv);
+                    for (int p = 0; p < 4; ++p) {
+                        const float v0 = v[2 * p] * kInv, v1 = v[2 * p + 1] * kInv;
+                        const uint16_t y0 = a.bf16 ? BF16::down(v0) : FP16::down(v0),
+                                       y1 = a.bf16 ? BF16::down(v1) : FP16::down(v1);
+                        y[p] = y0 | static_cast<uint32_t>(y1) << 16;
+                    }
+                    uint16_t *o = out + (a.tall ? j * a.ldo + i : i * a.ldo + j);
                     if (!a.tall && j + 8 <= c) {
-                        __builtin_memcpy(o + i * a.ldo + j, &y, 16);
+                        __builtin_memcpy(o, &y, 16);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (j + e < c) o[a.tall ? (j + e) * a.ldo + i : i * a.ldo + j + e] = y[e];
+                        for (int e = 0; e < 8; ++e, o += a.tall ? a.ldo : 1)
+                            if (j + e < c) *o = static_cast<uint16_t>(y[e / 2] >> (e & 1) * 16);
                     }
                 }
             }
         }
+    };
+    Square<R> square(wave, lane);
+#pragma unroll 1
+    for (int step = 0; step < a.steps; ++step) {
+        square.clear();
+#pragma unroll 1
+        for (int k = 0; k < C; k += 64) square.multiply(X, C, k);
+        square.put(A, diag);
+        __syncthreads();
+        square.polynomial(A, diag, a.coeffs[3 * step], a.coeffs[3 * step + 1],
+                          a.coeffs[3 * step + 2]);
+        if (step + 1 == a.steps) {
+            apply(std::true_type{});
+            return;
+        }
+        apply(std::false_type{});
         __syncthreads();
     }
 }
 
 // Up to 128 rows, too long for that: A and P by one workgroup a matrix in one
 // launch, from X itself in chunks that pass through shared memory, or (JOIN)
-// from the gram product's parts.  A launch less a round: 77 x 333 79 -> 71 us,
-// 64 x 2048 82 -> 66.
+// from the gram product's parts.  A launch less a round: 64 x 2048 82 -> 66
+// us, 77 x 333 (before one workgroup did all of it) 79 -> 71.
 constexpr int kChunk = 192;
 
 template <int R, bool JOIN>
