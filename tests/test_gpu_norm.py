@@ -230,6 +230,20 @@ def test_backward_of_each_split(n, xt, yt):
         check_backward(dy, x, w, mean, rstd, res, dx, dw, db)
 
 
+@pytest.mark.parametrize("m,n", [(8192, 4096), (8195, 3700), (8191, 4096), (6200, 1100),
+                                 (4099, 2304), (16400, 600)])
+@pytest.mark.parametrize("yt", [BF, F])
+def test_backward_of_many_rows(m, n, yt):
+    """one workgroup or two on a CU, one piece a lane or two"""
+    dy, x, w, mean, rstd, res, dx, dxbuf, dw, db, row = \
+        backward_case(gen(n + m), m, n, BF, BF, yt, F, True)
+    zs.zero_layernorm_backward(dy, x, w, mean, rstd, dx, residual=res, dw=dw, db=db)
+    check_backward(dy, x, w, mean, rstd, res, dx, dw, db)
+    part = dx.clone()
+    zs.zero_layernorm_backward(dy, x, w, mean, rstd, dx, residual=res)
+    assert torch.equal(part, dx)
+
+
 @pytest.mark.parametrize("m", [1, 7, 64, 511, 512, 513])
 @pytest.mark.parametrize("n", [8, 129, 1601, 5000, 9001, 16384])
 @pytest.mark.parametrize("gt", [BF, F])

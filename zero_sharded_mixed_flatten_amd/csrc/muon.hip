@@ -355,7 +355,8 @@ void run_update(const uint16_t *o, int64_t len, float *w, uint16_t *slot, float 
     const size_t lds = residency(20, len);
     for_launches(len, [&](int64_t at, int64_t n) {
         update_kernel<ODT, WDT>
-            <<<groups_of(n, skew_of(w)), kWave, lds, st>>>(o + at, n, w + at, slot + at, scale, skew_of(w), c, k);
+            <<<groups_of(n, skew_of(w)), kWave, lds, st>>>(o + at, n, w + at, slot + at, scale,
+                                                           skew_of(w), c, k);
     });
 }
 

@@ -785,19 +785,25 @@ zero_status launch_back(BackArgs a, void *stream) {
     const int64_t waves = ceil_div(a.n, 512);
     Grads how = grads ? SUMS : NONE;
     if (a.m > 0 && in_registers(a.n)) {
-        // One piece a lane up to 8192 elements, three or four beyond.  One
-        // workgroup on a CU keeps the column sums that go through memory few;
-        // two of them pay for 16-bit rows where those of one are less than
-        // eight waves' and each has rows enough (4096 x 2304 30.4 -> 25.7 us,
-        // 4096 x 4096 35.9 -> 37.3, 1023 x 2304 15.0 -> 15.3; fp32 3008 wide
-        // 43.7 -> 46.9).
-        const int W = static_cast<int>(std::min<int64_t>(waves <= kRowWaves ? kRowWaves : kBackWaves,
-                                                         waves));
+        // One piece a lane up to 8192 elements, three or four beyond; two of
+        // 16-bit rows that fill eight waves exactly, where there are many
+        // (4096 wide: 16384 rows 104 us for 119, 8192 60 for 64, 4096 37 for
+        // 36).  One workgroup on a CU keeps the column sums that go through
+        // memory few (16384 x 1600 fp32 82 us for two's 88, 4096 x 4500 42 for
+        // 47).  Two pay where x is 16-bit, each has rows enough, and one is
+        // short of eight waves (16384 x 2304 107 -> 70, with dy fp32 111 ->
+        // 81; 2048 x 3008 fp32 22 -> 24) or, with dy 16-bit too, has shorter
+        // rows (16384 x 1600 58 -> 51; with dy fp32 59 -> 60).
+        const bool twos = !XF && !DF && waves == kBackWaves && a.m >= 8192;
+        const int most = waves <= kRowWaves ? kRowWaves : kBackWaves;
+        const int W = static_cast<int>(twos ? kBackWaves / 2 : std::min<int64_t>(most, waves));
         const int R = std::max(1, kBackWaves / W);
         a.waves_a_row = W;
         const int64_t turns = ceil_div(a.m, R);
-        a.groups = static_cast<int32_t>(std::min<int64_t>(
-            !XF && !DF && W < kBackWaves && turns >= 4 * kGroups ? kGroups : kGroups / 2, turns));
+        const bool two = !XF && !twos && turns >= 4 * kGroups &&
+                         (W * R < kBackWaves || (!DF && W < kBackWaves));
+        a.groups =
+            static_cast<int32_t>(std::min<int64_t>(two ? kGroups : kGroups / 2, turns));
         const int threads = W * R * kWave;
         // One launch for two, which read x and dy twice: a row of 1600 7.3 ->
         // 3.0 us, 256 rows 10.7 -> 4.7, 512 10.7 -> 10.1, 1023 11.7 -> 17.8;
@@ -807,6 +813,9 @@ zero_status launch_back(BackArgs a, void *stream) {
         if (grads && a.m <= kFewRows && a.dx != a.dy) how = FEW;
         switch (ceil_div(waves, W)) {
             case 1: run_back<T, XF, DF, 1>(a, threads, how, st); break;
+            case 2:
+                if constexpr (!XF && !DF) run_back<T, XF, DF, 2>(a, threads, how, st);
+                break;
             case 3: run_back<T, XF, DF, 3>(a, threads, how, st); break;
             default: run_back<T, XF, DF, 4>(a, threads, how, st); break;
         }
