@@ -70,7 +70,8 @@ ZERO_API int64_t zero_layernorm_workspace_bytes(int64_t m, int64_t n);
  *         but not x.
  *   dw, db: n elements each of type gdt: wdt or FP32, or NULL.  Accumulation
  *         adds the fp32 sum to the widened old value and rounds once.  Without
- *         rows the sums are zero.
+ *         rows the sums are zero.  Equal calls give equal bits; the order of a
+ *         sum, and so its rounding, goes by sizes, types and whether dx is dy.
  * EINVAL as for zero_layernorm; also for a missing, unaligned or short
  * workspace when dw or db is given.  EALIAS: dx, dw, db or the workspace
  * overlaps anything else (dx == residual and dx == dy excepted). */
