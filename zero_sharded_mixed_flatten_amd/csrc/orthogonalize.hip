@@ -15,10 +15,32 @@
 // rounds amplify.  So the diagonals, where the large part of A and P lies, are
 // kept apart in fp32 and enter as row factors in fp32:
 //   A = D + O:  A A = O O + (d_i + d_j) O_ij + (d_i^2 on the diagonal)
-//   P = E + Q:  P X = e_i X_ij + Q X
-// with X itself held to 22 bits as hi + lo in the first term, and only O, Q
-// and hi are fp16 operands.  Measured against 64 bits over flat, decaying and
-// low-rank spectra: 1.2e-3 of the result's norm or less.
+//   P = E + Q:  P X = e_i hi_ij + f_i lo_ij + Q hi
+// with X itself held to 22 bits as hi + lo, and only O, Q and hi are fp16
+// operands.
+//
+// f, lo's factor, makes up for Q lo, which is left out: twice the apply.
+// Roundings that leave an error on one side of X's large directions only tilt
+// these a little.  lo is noise on both sides, 2^-12 of X in every direction,
+// and what the small directions get of it is multiplied with them, by the
+// coefficient a in every later round (3.4445^4 = 141 after the first).  With
+// f = a the error is (b A + c A A) lo, which the small directions, where b A +
+// c A A vanishes, get nothing of; with f = e_i it is Q lo, less where A is
+// mostly its diagonal, but noise in all directions where X has few and few rows
+// carry them.  So f is a in the rounds whose error would still be multiplied by
+// more than 4, and e_i in the others (of the usual five the last two), and in
+// all where there is one row.  Against 64 bits, usual rounds, bf16 to fp16, the
+// largest of 3 to 100 matrices a size and spectrum (flat, decaying, orthogonal,
+// one to eight directions over noise), in parentheses the largest median :
+// with e_i in all rounds:
+//   64 x 64 to 2048 x 2048                      1.8e-3 (1.8e-3) : 8.2e-3 (3.5e-3)
+//   16 x 16 to 32 x 32                          2.8e-3 (2.6e-3) : 2.1e-2 (1.1e-2)
+//   one direction in 2 to 16 of 64 rows or more 2.1e-3 (1.4e-3) : 4.4e-2 (3.0e-2)
+//   the same in as few of the columns           4.7e-3 (1.8e-3) : 5.4e-2 (2.2e-2)
+//   5 x 9, 8 x 8                                4.4e-3 (1.9e-3) : 3.3e-2 (1.7e-2)
+//   2 x 2 to 3 x 7                              8.8e-3 (1.9e-3) : 4.5e-2 (1.7e-2)
+// where bf16's own rounding of the result is 1.7e-3.  Few rows' roundings do
+// not average out, and the polynomial's slope multiplies them.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -261,6 +283,7 @@ struct Args {
     int32_t rp, cp;
     int32_t tiles, tiles_i, tiles_j, count;
     int32_t parts, part_steps;  // gram
+    int32_t lo_diagonal;        // apply: lo's factor is e_i, else ca
     int32_t whole;   // tiles of 256 that the launch has, or
     int32_t quarter; // >= 0: the workgroups are quarters of those from here on
     f32x4 *partial;
@@ -639,7 +662,7 @@ __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kerne
                 const int u = group * GROUP + k, f = u / (FJ / 2), p = u % (FJ / 2);
                 if (!mine(u)) continue;
                 const u16x8 hi = xh[group & 1][k];
-                const float ri = ei[group & 1][k];
+                const float ri = ei[group & 1][k], fi = a.lo_diagonal ? ri : a.ca;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     float v = acc[f][2 * p + e / 4][e & 3];
@@ -651,7 +674,8 @@ __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kerne
                                      : __builtin_fmaf(a.cc, sq, a.cb * oij) * kScale;
                     } else {
                         const u16x8 lo = xl[group & 1][k];
-                        v = __builtin_fmaf(ri, FP16::up(hi[e]) + FP16::up(lo[e]), v * kInv);
+                        const float rest = __builtin_fmaf(fi, FP16::up(lo[e]), v * kInv);
+                        v = __builtin_fmaf(ri, FP16::up(hi[e]), rest);
                     }
                     acc[f][2 * p + e / 4][e & 3] = v;
                 }
@@ -801,6 +825,7 @@ struct SmallArgs {
     int64_t ldo, so;
     double eps;
     int32_t cp, steps, tall, bf16;
+    uint32_t lo_diagonal;  // the rounds, a bit each, where lo's factor is e_i
     float coeffs[3 * ZERO_NS_MAX_STEPS];
 };
 
@@ -825,6 +850,10 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
     __shared__ __attribute__((aligned(128))) uint16_t X[R * kSmallColumns<R>];
     __shared__ __attribute__((aligned(128))) uint16_t A[R * R];
     __shared__ float diag[R];
+    // lo's factor of each round, as 1 e_i + 0 or 0 e_i + a.  From shared memory:
+    // the compiler makes a choice two copies of the loops, and has no scalar
+    // register left for more arguments (either 3 x 77 x 333 66 us for 60).
+    __shared__ float lo_terms[ZERO_NS_MAX_STEPS][2];
     __shared__ double wave_part[kSmallWaves];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -832,6 +861,11 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
     const int C = a.cp;
     const int r = a.tall ? a.in.cols : a.in.rows, c = a.tall ? a.in.rows : a.in.cols;
     uint16_t *lo = a.lo + m * R * C;
+    if (tid < a.steps) {
+        const bool diagonal = a.lo_diagonal >> tid & 1;
+        lo_terms[tid][0] = diagonal ? 1.0f : 0.0f;
+        lo_terms[tid][1] = diagonal ? 0.0f : a.coeffs[3 * tid];
+    }
 
     // |U|^2: whole pieces, kAhead of them under way, then the rows' ends
     double s = 0.0;
@@ -934,7 +968,7 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
     // one to read and to write them.  The last time it is the result; a copy of
     // the code of its own, or its conversions are made every time.
     uint16_t *const out = static_cast<uint16_t *>(a.o) + m * a.so;
-    const auto apply = [&](auto last) __attribute__((always_inline)) {
+    const auto apply = [&](auto last, float share, float rest) __attribute__((always_inline)) {
 #pragma unroll 1
         for (int j0 = wave * 32; j0 < C; j0 += kSmallWaves * 32) {
             const int j = j0 + g * 8;
@@ -983,12 +1017,12 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
                 }
                 uint16_t *xp = X + piece_of(i, C, j / 8);
                 const u32x4 h = xh[f % G];
-                const float e_i = d[f % G];
+                const float e_i = d[f % G], f_i = __builtin_fmaf(share, e_i, rest);
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     v[e] = __builtin_fmaf(pair(h, e / 2)[e & 1], e_i,
-                                          __builtin_fmaf(pair(l[f], e / 2)[e & 1], e_i,
+                                          __builtin_fmaf(pair(l[f], e / 2)[e & 1], f_i,
                                                          x[f][e / 4][e & 3] * kInv));
                 if constexpr (!decltype(last)::value) {
                     u32x4 nh, nl;
@@ -1027,10 +1061,10 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
         square.polynomial(A, diag, a.coeffs[3 * step], a.coeffs[3 * step + 1],
                           a.coeffs[3 * step + 2]);
         if (step + 1 == a.steps) {
-            apply(std::true_type{});
+            apply(std::true_type{}, lo_terms[step][0], lo_terms[step][1]);
             return;
         }
-        apply(std::false_type{});
+        apply(std::false_type{}, lo_terms[step][0], lo_terms[step][1]);
         __syncthreads();
     }
 }
@@ -1323,6 +1357,19 @@ void run_small(const SmallArgs &a, int64_t rp, int64_t count, hipStream_t st) {
         small_kernel<DT, 128><<<n, kSmallWaves * kWave, 0, st>>>(a);
 }
 
+// The rounds, a bit each, whose error in lo's place small directions multiply
+// by 4 at most until the end, by the coefficients a of the rounds that follow:
+// there lo's factor is the diagonal of P (see above).
+uint32_t diagonal_rounds(const double *coeffs, int32_t steps, int64_t r) {
+    uint32_t rounds = 0;
+    double slope = 1.0;
+    for (int32_t i = steps - 1; i >= 0; --i) {
+        if (slope <= 4.0 || r == 1) rounds |= uint32_t(1) << i;
+        slope *= std::fabs(coeffs[3 * i]);
+    }
+    return rounds;
+}
+
 // a stack of count matrices: the span of all, and whether its strides hold
 bool stack_ok(const Mat &one, int64_t count, int64_t stride, Span *all) {
     if (!one.ok()) return false;
@@ -1376,12 +1423,14 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     const bool tall = rows > cols;
     const Input in{u, ldu, su, static_cast<int32_t>(rows), static_cast<int32_t>(cols)};
     const double usual_coeffs[3] = {3.4445, -4.7750, 2.0315};
+    double coeffs[3 * ZERO_NS_MAX_STEPS];
+    for (int i = 0; i < 3 * k.steps; ++i)
+        coeffs[i] = k.coeffs != nullptr ? k.coeffs[i] : usual_coeffs[i % 3];
+    const uint32_t lo_diagonal = diagonal_rounds(coeffs, k.steps, w.r);
     if (is_small(w)) {
         SmallArgs a{in, reinterpret_cast<uint16_t *>(ws + w.lo), o, ldo, so, k.eps,
-                    static_cast<int32_t>(w.cp), k.steps, tall, odt == ZERO_BF16, {}};
-        for (int i = 0; i < 3 * k.steps; ++i)
-            a.coeffs[i] =
-                static_cast<float>(k.coeffs != nullptr ? k.coeffs[i] : usual_coeffs[i % 3]);
+                    static_cast<int32_t>(w.cp), k.steps, tall, odt == ZERO_BF16, lo_diagonal, {}};
+        for (int i = 0; i < 3 * k.steps; ++i) a.coeffs[i] = static_cast<float>(coeffs[i]);
         if (udt == ZERO_BF16)
             run_small<ZERO_BF16>(a, w.rp, count, st);
         else if (udt == ZERO_FP16)
@@ -1418,7 +1467,7 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     const Way gram = way_of(GRAM, w, count);
     zero_status status = launch_status();
     for (int i = 0; i < k.steps && status == ZERO_OK; ++i) {
-        const double *c = k.coeffs != nullptr ? k.coeffs + 3 * i : usual_coeffs;
+        const double *c = coeffs + 3 * i;
         const uint16_t *x = hi[i & 1];
         Args g = base;
         g.p = g.q = x;
@@ -1452,6 +1501,8 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
         p.out = hi[(i + 1) & 1];
         p.out_lo = lo;
         p.diag = e;
+        p.ca = static_cast<float>(c[0]);
+        p.lo_diagonal = lo_diagonal >> i & 1;
         status = i + 1 < k.steps ? run<APPLY>(p, w, st) : run<FINISH>(p, w, st);
     }
     return status;
