@@ -100,3 +100,22 @@ def test_rounds_whose_slope_is_not_the_usual():
                  torch.randn(1, c, generator=g, device="cuda") +
                  1e-4 * torch.randn(r, c, generator=g, device="cuda")).to(BF)
             check(u, r, str(coeffs[0]), 1.6, steps=len(coeffs), coeffs=coeffs)
+
+
+LARGE = [([(1.5, 0.0, 0.0)] * 6, 1.0),                      # singular value 11.4
+         ([(6.0, 0.0, 0.0), (0.2, 0.0, 0.0)], 1.0),
+         ([(15.5, 0.0, 0.0), (0.05, 0.0, 0.0)], 1.0),
+         ([(12.0, 0.0, 0.0), (0.5, -0.004, 1e-5)], 1.0),
+         ([(61.0, -60.0, 0.0), (1.0, 0.0, 0.0)], 60 / 2.81)]  # an off-diagonal of P is -30
+
+
+@pytest.mark.parametrize("coeffs,rounds", LARGE)
+@pytest.mark.parametrize("r,c", [(1, 1), (2, 2), (64, 64), (30, 1000), (128, 448), (100, 700),
+                                 (128, 2000), (40, 1500), (200, 300), (300, 520), (1024, 1024)])
+def test_singular_values_up_to_the_documented_limit(r, c, coeffs, rounds):
+    """all of the matrix in two rows: the off-diagonals of A are half the square of
+    the singular value.  An error is multiplied by |b s^2 + c s^4| as far as that
+    is larger than the usual."""
+    u = torch.zeros(r, c, device="cuda")
+    u[:2] = torch.rand(1, c, generator=gen(c), device="cuda") + 0.5
+    check(u.to(BF), 2, str(coeffs), rounds, steps=len(coeffs), coeffs=coeffs)

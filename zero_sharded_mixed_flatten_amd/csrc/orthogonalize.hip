@@ -9,7 +9,10 @@
 //   apply   X = P X
 // Rounding.  fp16 keeps 11 bits where bf16 keeps 8, at the same rate; every
 // value here is scaled by 2^12, which leaves room up to 16 above and down to
-// 2^-26 below at full precision.  Rounding A, P or X as a whole would cost a
+// 2^-26 below at full precision.  X has that room by contract; A's and P's
+// off-diagonals, up to half the square of X's largest singular value and half
+// the spread of b s^2 + c s^4, are scaled by less where the coefficients could
+// let them need more (rounds_of).  Rounding A, P or X as a whole would cost a
 // few times 2^-11 of the result where singular values are alike, and all of
 // its small singular directions where they are not, since those are what the
 // rounds amplify.  So the diagonals, where the large part of A and P lies, are
@@ -269,6 +272,13 @@ __global__ void __launch_bounds__(256) spread_kernel(Input in, const double *par
 // ---------------------------------------------------------------------------
 // the products
 
+// Powers of two: A's off-diagonals in fp16 from a product of X, scaled by 2^24,
+// and back, and P's.
+struct Scales {
+    float to_a, from_a, from_aa;  // from_aa: from a product of two A
+    float to_p, from_p;
+};
+
 enum Kind { GRAM = 0, SQUARE = 1, APPLY = 2, FINISH = 3 };  // FINISH: the last apply
 
 struct Args {
@@ -288,6 +298,7 @@ struct Args {
     int32_t quarter; // >= 0: the workgroups are quarters of those from here on
     f32x4 *partial;
     float ca, cb, cc;
+    Scales scale;
     int32_t tall, bf16;
 };
 
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kerne
             for (int e = 0; e < 8; ++e) {
                 const bool diagonal = ti == tj && i == j + e;
                 if (diagonal) a.new_diag[pd + i0 + i] = KIND == GRAM ? v[e] * kInv2 : v[e];
-                h[e] = diagonal ? 0 : FP16::down(KIND == GRAM ? v[e] * kInv : v[e]);
+                h[e] = diagonal ? 0 : FP16::down(KIND == GRAM ? v[e] * a.scale.to_a : v[e]);
             }
             *reinterpret_cast<u16x8 *>(tile + offset(i, j)) = h;
             if (ti != tj) {
@@ -667,14 +678,16 @@ __global__ void __launch_bounds__(WI *WJ *KG *kWave, JOIN ? 1 : 2) product_kerne
                 for (int e = 0; e < 8; ++e) {
                     float v = acc[f][2 * p + e / 4][e & 3];
                     if constexpr (KIND == SQUARE) {
-                        const float oo = v * kInv2, oij = FP16::up(hi[e]) * kInv;
+                        const float oo = v * a.scale.from_aa,
+                                    oij = FP16::up(hi[e]) * a.scale.from_a;
                         const float sq = __builtin_fmaf(ri + dj[2 * p + e / 4][e & 3], oij, oo);
                         const bool diagonal = ti == tj && row_of(u) == column_of(u) + e;
                         v = diagonal ? a.ca + a.cb * ri + a.cc * (oo + ri * ri)
-                                     : __builtin_fmaf(a.cc, sq, a.cb * oij) * kScale;
+                                     : __builtin_fmaf(a.cc, sq, a.cb * oij) * a.scale.to_p;
                     } else {
                         const u16x8 lo = xl[group & 1][k];
-                        const float rest = __builtin_fmaf(fi, FP16::up(lo[e]), v * kInv);
+                        const float rest =
+                            __builtin_fmaf(fi, FP16::up(lo[e]), v * a.scale.from_p);
                         v = __builtin_fmaf(ri, FP16::up(hi[e]), rest);
                     }
                     acc[f][2 * p + e / 4][e & 3] = v;
@@ -772,7 +785,7 @@ struct Square {
                 for (int b = 0; b < 2; ++b) acc[f][b] = mfma<FP16>(q[h][b], p[h][f], acc[f][b]);
     }
     // acc is X X^T: its diagonal to diag, the rest to A in shared memory
-    __device__ __forceinline__ void put(uint16_t *A, float *diag) {
+    __device__ __forceinline__ void put(uint16_t *A, float *diag, float to_a) {
 #pragma unroll
         for (int f = 0; f < FI; ++f) {
             const int i = row(f);
@@ -781,7 +794,7 @@ struct Square {
             for (int e = 0; e < 8; ++e) {
                 v[e] = acc[f][e / 4][e & 3];
                 if (i == j + e) diag[i] = v[e] * kInv2;
-                v[e] = i == j + e ? 0.0f : v[e] * kInv;
+                v[e] = i == j + e ? 0.0f : v[e] * to_a;
             }
             own[f] = pack(v);
             *reinterpret_cast<u32x4 *>(A + piece_of(i, R, j / 8)) = own[f];
@@ -790,7 +803,7 @@ struct Square {
     // A and its diagonal become P = a + b A + c A A and its diagonal; all waves
     // see A before, and P after it
     __device__ __forceinline__ void polynomial(uint16_t *A, float *diag, float ca, float cb,
-                                               float cc) {
+                                               float cc, const Scales scale) {
         clear();
 #pragma unroll
         for (int k = 0; k < R; k += 64) multiply(A, R, k);
@@ -806,16 +819,22 @@ struct Square {
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float oo = acc[f][e / 4][e & 3] * kInv2;
-                const float oij = pair(own[f], e / 2)[e & 1] * kInv;
+                const float oo = acc[f][e / 4][e & 3] * scale.from_aa;
+                const float oij = pair(own[f], e / 2)[e & 1] * scale.from_a;
                 const float sq = __builtin_fmaf(di[f] + dj[e], oij, oo);
                 if (i == j + e) diag[i] = ca + cb * di[f] + cc * (oo + di[f] * di[f]);
-                v[e] = i == j + e ? 0.0f : __builtin_fmaf(cc, sq, cb * oij) * kScale;
+                v[e] = i == j + e ? 0.0f : __builtin_fmaf(cc, sq, cb * oij) * scale.to_p;
             }
             *reinterpret_cast<u32x4 *>(A + piece_of(i, R, j / 8)) = pack(v);
         }
         __syncthreads();
     }
+};
+
+struct Round {
+    float a, b, c;
+    float lo_share, lo_rest;  // lo's factor, as 1 e_i + 0 or 0 e_i + a
+    Scales scale;
 };
 
 struct SmallArgs {
@@ -825,8 +844,7 @@ struct SmallArgs {
     int64_t ldo, so;
     double eps;
     int32_t cp, steps, tall, bf16;
-    uint32_t lo_diagonal;  // the rounds, a bit each, where lo's factor is e_i
-    float coeffs[3 * ZERO_NS_MAX_STEPS];
+    Round rounds[ZERO_NS_MAX_STEPS];
 };
 
 template <int R>
@@ -850,10 +868,10 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
     __shared__ __attribute__((aligned(128))) uint16_t X[R * kSmallColumns<R>];
     __shared__ __attribute__((aligned(128))) uint16_t A[R * R];
     __shared__ float diag[R];
-    // lo's factor of each round, as 1 e_i + 0 or 0 e_i + a.  From shared memory:
-    // the compiler makes a choice two copies of the loops, and has no scalar
-    // register left for more arguments (either 3 x 77 x 333 66 us for 60).
-    __shared__ float lo_terms[ZERO_NS_MAX_STEPS][2];
+    // From shared memory, not the arguments: the compiler has no scalar register
+    // left for them (3 x 77 x 333 66 us for 60.5, and so with a choice of lo's
+    // factor in the loops, which it makes two copies of).
+    __shared__ Round rounds[ZERO_NS_MAX_STEPS];
     __shared__ double wave_part[kSmallWaves];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -861,11 +879,7 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
     const int C = a.cp;
     const int r = a.tall ? a.in.cols : a.in.rows, c = a.tall ? a.in.rows : a.in.cols;
     uint16_t *lo = a.lo + m * R * C;
-    if (tid < a.steps) {
-        const bool diagonal = a.lo_diagonal >> tid & 1;
-        lo_terms[tid][0] = diagonal ? 1.0f : 0.0f;
-        lo_terms[tid][1] = diagonal ? 0.0f : a.coeffs[3 * tid];
-    }
+    if (tid < a.steps) rounds[tid] = a.rounds[tid];
 
     // |U|^2: whole pieces, kAhead of them under way, then the rows' ends
     double s = 0.0;
@@ -968,7 +982,8 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
     // one to read and to write them.  The last time it is the result; a copy of
     // the code of its own, or its conversions are made every time.
     uint16_t *const out = static_cast<uint16_t *>(a.o) + m * a.so;
-    const auto apply = [&](auto last, float share, float rest) __attribute__((always_inline)) {
+    const auto apply = [&](auto last, float share, float rest,
+                           float from_p) __attribute__((always_inline)) {
 #pragma unroll 1
         for (int j0 = wave * 32; j0 < C; j0 += kSmallWaves * 32) {
             const int j = j0 + g * 8;
@@ -1023,7 +1038,7 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
                 for (int e = 0; e < 8; ++e)
                     v[e] = __builtin_fmaf(pair(h, e / 2)[e & 1], e_i,
                                           __builtin_fmaf(pair(l[f], e / 2)[e & 1], f_i,
-                                                         x[f][e / 4][e & 3] * kInv));
+                                                         x[f][e / 4][e & 3] * from_p));
                 if constexpr (!decltype(last)::value) {
                     u32x4 nh, nl;
                     split8(v, nh, nl);
@@ -1056,15 +1071,20 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) small_kernel(SmallArgs a) 
         square.clear();
 #pragma unroll 1
         for (int k = 0; k < C; k += 64) square.multiply(X, C, k);
-        square.put(A, diag);
+        // each constant is read where it is used, and in either branch: held any
+        // longer, the registers it takes make the compiler of 128 rows read one
+        // operand at a time (3 x 77 x 333 65 us for 60.5)
+        square.put(A, diag, rounds[step].scale.to_a);
         __syncthreads();
-        square.polynomial(A, diag, a.coeffs[3 * step], a.coeffs[3 * step + 1],
-                          a.coeffs[3 * step + 2]);
+        square.polynomial(A, diag, a.rounds[step].a, a.rounds[step].b, a.rounds[step].c,
+                          rounds[step].scale);
         if (step + 1 == a.steps) {
-            apply(std::true_type{}, lo_terms[step][0], lo_terms[step][1]);
+            apply(std::true_type{}, rounds[step].lo_share, rounds[step].lo_rest,
+                  rounds[step].scale.from_p);
             return;
         }
-        apply(std::false_type{}, lo_terms[step][0], lo_terms[step][1]);
+        apply(std::false_type{}, rounds[step].lo_share, rounds[step].lo_rest,
+              rounds[step].scale.from_p);
         __syncthreads();
     }
 }
@@ -1113,7 +1133,7 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) narrow_kernel(Args a) {
                 for (int e = 0; e < 8; ++e) {
                     v[e] = sum[f][e / 4][e & 3];
                     if (i == j + e) diag[i] = v[e] * kInv2;
-                    v[e] = i == j + e ? 0.0f : v[e] * kInv;
+                    v[e] = i == j + e ? 0.0f : v[e] * a.scale.to_a;
                 }
                 *reinterpret_cast<u32x4 *>(A + piece_of(i, R, j / 8)) = pack(v);
                 if (ti != tj) {
@@ -1156,10 +1176,10 @@ __global__ void __launch_bounds__(kSmallWaves *kWave) narrow_kernel(Args a) {
             for (int k = 0; k < kChunk; k += 64)
                 if (k < left) square.multiply(X, kChunk, k);
         }
-        square.put(A, diag);
+        square.put(A, diag, a.scale.to_a);
         __syncthreads();
     }
-    square.polynomial(A, diag, a.ca, a.cb, a.cc);
+    square.polynomial(A, diag, a.ca, a.cb, a.cc, a.scale);
     uint16_t *out = a.out + m * R * R;
     for (int p = tid; p < R * R / 8; p += THREADS) {
         const int i = p / (R / 8), s = p % (R / 8);
@@ -1357,17 +1377,58 @@ void run_small(const SmallArgs &a, int64_t rp, int64_t count, hipStream_t st) {
         small_kernel<DT, 128><<<n, kSmallWaves * kWave, 0, st>>>(a);
 }
 
-// The rounds, a bit each, whose error in lo's place small directions multiply
-// by 4 at most until the end, by the coefficients a of the rounds that follow:
-// there lo's factor is the diagonal of P (see above).
-uint32_t diagonal_rounds(const double *coeffs, int32_t steps, int64_t r) {
-    uint32_t rounds = 0;
-    double slope = 1.0;
-    for (int32_t i = steps - 1; i >= 0; --i) {
-        if (slope <= 4.0 || r == 1) rounds |= uint32_t(1) << i;
-        slope *= std::fabs(coeffs[3 * i]);
+// the largest power of two up to kScale that keeps magnitudes of `most` well
+// inside fp16's range
+double scale_for(double most) {
+    return std::ldexp(1.0, static_cast<int>(std::min(
+                               12.0, std::max(-100.0, std::floor(15.0 - std::log2(most))))));
+}
+
+// Each round's constants.  `top` bounds X's singular values: 1 at first, then
+// what the polynomial makes of those up to it (1 % more for its roundings), and
+// 16 by contract.  Off-diagonal elements of a symmetric matrix are at most half
+// the difference of two of its eigenvalues.  lo's factor is the diagonal of P
+// in the rounds whose error small directions multiply by 4 at most until the
+// end, by the coefficients a of the rounds that follow, and a in the others.
+void rounds_of(const zero_ns_params &k, int64_t r, Round *rounds) {
+    const double usual[3] = {3.4445, -4.7750, 2.0315};
+    double top = 1.01;
+    for (int i = 0; i < k.steps; ++i) {
+        const double *given = k.coeffs != nullptr ? k.coeffs + 3 * i : usual;
+        Round &q = rounds[i];
+        q.a = static_cast<float>(given[0]);
+        q.b = static_cast<float>(given[1]);
+        q.c = static_cast<float>(given[2]);
+        const double a = q.a, b = q.b, c = q.c, t1 = top * top;
+        // b t + c t^2 over t = s^2 up to top^2
+        const double end = t1 * (b + c * t1), turn = -b / (2.0 * c);
+        double low = std::min(0.0, end), high = std::max(0.0, end);
+        if (turn > 0.0 && turn < t1) {
+            low = std::min(low, 0.5 * b * turn);
+            high = std::max(high, 0.5 * b * turn);
+        }
+        const double scale_a = scale_for(0.5 * t1), scale_p = scale_for(0.5 * (high - low));
+        q.scale.to_a = static_cast<float>(scale_a / (4096.0 * 4096.0));
+        q.scale.from_a = static_cast<float>(1.0 / scale_a);
+        q.scale.from_aa = static_cast<float>(1.0 / (scale_a * scale_a));
+        q.scale.to_p = static_cast<float>(scale_p);
+        q.scale.from_p = static_cast<float>(1.0 / scale_p);
+        // the largest |s (a + b s^2 + c s^4)|: at the end, or where 5 c t^2 + 3 b
+        // t + a is zero
+        double next = top * std::fabs(a + end);
+        const double root = std::sqrt(9.0 * b * b - 20.0 * a * c);
+        for (double t : {(-3.0 * b - root) / (10.0 * c), (-3.0 * b + root) / (10.0 * c),
+                         -a / (3.0 * b)})
+            if (t > 0.0 && t < t1) next = std::max(next, std::sqrt(t) * std::fabs(a + t * (b + c * t)));
+        top = std::min(16.0, 1.01 * next);
     }
-    return rounds;
+    double slope = 1.0;
+    for (int i = k.steps - 1; i >= 0; --i) {
+        const bool diagonal = slope <= 4.0 || r == 1;
+        rounds[i].lo_share = diagonal ? 1.0f : 0.0f;
+        rounds[i].lo_rest = diagonal ? 0.0f : rounds[i].a;
+        slope *= std::fabs(rounds[i].a);
+    }
 }
 
 // a stack of count matrices: the span of all, and whether its strides hold
@@ -1422,15 +1483,10 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     char *ws = static_cast<char *>(workspace);
     const bool tall = rows > cols;
     const Input in{u, ldu, su, static_cast<int32_t>(rows), static_cast<int32_t>(cols)};
-    const double usual_coeffs[3] = {3.4445, -4.7750, 2.0315};
-    double coeffs[3 * ZERO_NS_MAX_STEPS];
-    for (int i = 0; i < 3 * k.steps; ++i)
-        coeffs[i] = k.coeffs != nullptr ? k.coeffs[i] : usual_coeffs[i % 3];
-    const uint32_t lo_diagonal = diagonal_rounds(coeffs, k.steps, w.r);
     if (is_small(w)) {
         SmallArgs a{in, reinterpret_cast<uint16_t *>(ws + w.lo), o, ldo, so, k.eps,
-                    static_cast<int32_t>(w.cp), k.steps, tall, odt == ZERO_BF16, lo_diagonal, {}};
-        for (int i = 0; i < 3 * k.steps; ++i) a.coeffs[i] = static_cast<float>(coeffs[i]);
+                    static_cast<int32_t>(w.cp), k.steps, tall, odt == ZERO_BF16, {}};
+        rounds_of(k, w.r, a.rounds);
         if (udt == ZERO_BF16)
             run_small<ZERO_BF16>(a, w.rp, count, st);
         else if (udt == ZERO_FP16)
@@ -1465,10 +1521,16 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     base.bf16 = odt == ZERO_BF16;
     base.partial = reinterpret_cast<f32x4 *>(ws + w.partial);
     const Way gram = way_of(GRAM, w, count);
+    Round rounds[ZERO_NS_MAX_STEPS];
+    rounds_of(k, w.r, rounds);
     zero_status status = launch_status();
     for (int i = 0; i < k.steps && status == ZERO_OK; ++i) {
-        const double *c = coeffs + 3 * i;
+        const Round &round = rounds[i];
         const uint16_t *x = hi[i & 1];
+        base.ca = round.a;
+        base.cb = round.b;
+        base.cc = round.c;
+        base.scale = round.scale;
         Args g = base;
         g.p = g.q = x;
         g.out = A;
@@ -1478,9 +1540,6 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
         s.out = Q;
         s.diag = d;
         s.new_diag = e;
-        s.ca = static_cast<float>(c[0]);
-        s.cb = static_cast<float>(c[1]);
-        s.cc = static_cast<float>(c[2]);
         const bool divided = gram.parts > 1;
         if (w.rp > 128 || divided) status = run<GRAM>(g, w, st);
         if (status != ZERO_OK) break;
@@ -1501,8 +1560,7 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
         p.out = hi[(i + 1) & 1];
         p.out_lo = lo;
         p.diag = e;
-        p.ca = static_cast<float>(c[0]);
-        p.lo_diagonal = lo_diagonal >> i & 1;
+        p.lo_diagonal = round.lo_share != 0.0f;
         status = i + 1 < k.steps ? run<APPLY>(p, w, st) : run<FINISH>(p, w, st);
     }
     return status;
