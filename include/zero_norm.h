@@ -33,7 +33,9 @@ extern "C" {
  *   rstd = 1 / sqrt(var + eps), y = (x - mean) * rstd * w + b.
  * The variance is centred: the row is held while its mean is formed, and its
  * differences are what is squared.  A row with an Inf or a NaN gives NaN
- * throughout; no other row is affected.
+ * throughout; no other row is affected.  In a row of finite values so large
+ * that the sum of the squared differences passes fp32's range rstd is 0 and y
+ * is b; one whose sum or differences do is NaN.
  *   x:    type xdt: wdt or FP32 (an fp32 residual stream).
  *   w, b: n elements of type wdt (BF16 or FP16); NULL for ones, and zeros.
  *   y:    type ydt: wdt or FP32.  It may be x itself (the same address, type

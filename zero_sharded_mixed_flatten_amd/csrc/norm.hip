@@ -209,8 +209,10 @@ inline bool in_registers(int64_t n) { return n >= 8 && n <= kLimit; }
 __device__ __forceinline__ float finish_row(float s1, float s2, float n, float eps, float &rest) {
     rest = s1 / n;
     const float var = fmaxf(s2 / n - rest * rest, 0.0f);
-    // fmaxf drops a NaN: s2 is one where the row holds an Inf or a NaN
-    return s2 != s2 ? s2 : 1.0f / sqrtf(var + eps);
+    // fmaxf drops a NaN: s2 is one where the row holds an Inf or a NaN, and Inf
+    // less Inf is one where only the squares pass fp32's range
+    if (s2 != s2) return s2;
+    return s2 == __builtin_inff() ? 0.0f : 1.0f / sqrtf(var + eps);
 }
 
 // W waves of a workgroup share a row, or (W = 1, K = 1) a wave has 64 / L
