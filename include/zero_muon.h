@@ -124,7 +124,8 @@ ZERO_API zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t l
  * weight_full[rank * shard + shard_off + j].
  *   o:     device, len elements of type odt (BF16 or FP16): the range's part
  *          of zero_orthogonalize's result.
- *   Everything else as for zero_shard_adamw, update_scale finite. */
+ *   Everything else as for zero_shard_adamw, update_scale finite as
+ *   an fp32 value. */
 ZERO_API zero_status zero_muon_update(const void *o, zero_dtype odt, float *master,
                                       void *weight_full, zero_dtype wdt,
                                       const zero_layout *layout, int32_t rank, int64_t shard_off,

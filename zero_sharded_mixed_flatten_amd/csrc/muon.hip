@@ -366,7 +366,8 @@ zero_status update_impl(const void *o, zero_dtype odt, float *master, void *weig
                         const zero_step_consts *dc, double update_scale, const uint32_t *skip,
                         void *stream) {
     if (!dtype_ok(odt) || !dtype_ok(wdt) || !layout_ok(layout)) return ZERO_EINVAL;
-    if (!(dc ? aligned8(dc) : hparams_ok(hp)) || !std::isfinite(update_scale)) return ZERO_EINVAL;
+    const float scale = static_cast<float>(update_scale);
+    if (!(dc ? aligned8(dc) : hparams_ok(hp)) || !std::isfinite(scale)) return ZERO_EINVAL;
     if (rank < 0 || rank >= layout->n_dp || shard_off < 0 || len < 0 || len > kMaxLen)
         return ZERO_EINVAL;
     if (shard_off > layout->shard || len > layout->shard - shard_off) return ZERO_ERANGE;
@@ -383,7 +384,6 @@ zero_status update_impl(const void *o, zero_dtype odt, float *master, void *weig
         if (overlap(sw, r) || overlap(ss, r)) return ZERO_EALIAS;
     const Consts c = dc ? Consts{} : make_consts(*hp);
     const Control k{skip, nullptr, 0.0, nullptr, 0.0, dc};
-    const float scale = static_cast<float>(update_scale);
     const auto *in = static_cast<const uint16_t *>(o);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (odt == ZERO_BF16)
