@@ -1459,7 +1459,8 @@ zero_status zero_orthogonalize(const void *u, zero_dtype udt, int64_t ldu, int64
     const zero_ns_params &k = ns != nullptr ? *ns : usual;
     if ((!is16(udt) && udt != ZERO_FP32) || !is16(odt) || !sides_ok(count, rows, cols))
         return ZERO_EINVAL;
-    if (k.steps < 1 || k.steps > ZERO_NS_MAX_STEPS || !(std::isfinite(k.eps) && k.eps >= 0.0))
+    if (k.steps < 1 || k.steps > ZERO_NS_MAX_STEPS || k.reserved != 0 ||
+        !(std::isfinite(k.eps) && k.eps >= 0.0))
         return ZERO_EINVAL;
     for (int i = 0; k.coeffs != nullptr && i < 3 * k.steps; ++i)
         if (!std::isfinite(static_cast<float>(k.coeffs[i]))) return ZERO_EINVAL;
