@@ -1201,6 +1201,11 @@ struct Work {
 
 int64_t partial_bytes(const Work &w, int64_t count);
 
+// by one workgroup a matrix, to which only X's lo is not local
+bool is_small(const Work &w) {
+    return w.rp == 64 ? w.cp <= kSmallColumns<64> : w.rp == 128 && w.cp <= kSmallColumns<128>;
+}
+
 Work work_of(int64_t count, int64_t rows, int64_t cols) {
     Work w{};
     w.r = std::min(rows, cols);
@@ -1213,6 +1218,11 @@ Work work_of(int64_t count, int64_t rows, int64_t cols) {
         at += (bytes + 255) / 256 * 256;
         return here;
     };
+    if (is_small(w)) {
+        w.lo = take(count * w.rp * w.cp * 2);
+        w.bytes = at;
+        return w;
+    }
     w.parts = take(count * kParts * 8);
     w.d = take(count * w.rp * 4);
     w.e = take(count * w.rp * 4);
@@ -1362,10 +1372,6 @@ void run_narrow(const Args &a, bool join, hipStream_t st) {
     else
         join ? narrow_kernel<128, true><<<n, kSmallWaves * kWave, 0, st>>>(a)
              : narrow_kernel<128, false><<<n, kSmallWaves * kWave, 0, st>>>(a);
-}
-
-bool is_small(const Work &w) {
-    return w.rp == 64 ? w.cp <= kSmallColumns<64> : w.rp == 128 && w.cp <= kSmallColumns<128>;
 }
 
 template <int DT>
