@@ -1,5 +1,6 @@
-"""The layer norm of finite rows whose squares pass fp32's range: 1 / sqrt of
-an infinite variance is 0, so y is the bias (or 0), as fp32 arithmetic has it."""
+"""The layer norm at the edges of its domain.  Finite rows whose squares pass
+fp32's range: 1 / sqrt of an infinite variance is 0, so y is the bias (or 0), as
+fp32 arithmetic has it.  Calls whose 16-bit type only the gradients tell."""
 import pytest
 import torch
 
@@ -43,3 +44,22 @@ def test_a_sum_beyond_the_range_is_nan(n):
     y, rstd = torch.empty(3, n, device="cuda"), torch.empty(3, device="cuda")
     zs.zero_layernorm(x, None, None, y, rstd=rstd)
     assert y[1].isnan().all() and (y[[0, 2]] == 0).all()
+
+
+@pytest.mark.parametrize("gt", [BF, torch.float16])
+def test_gradients_in_16_bits_of_fp32_rows_without_a_weight(gt):
+    """the gradient row's type is then the only 16-bit one of the call"""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    m, n = 40, 300
+    x, dy = (torch.randn(m, n, generator=g, device="cuda") for _ in range(2))
+    mean, rstd = torch.empty(m, device="cuda"), torch.empty(m, device="cuda")
+    zs.zero_layernorm(x, None, None, torch.empty_like(x), mean=mean, rstd=rstd)
+    dx, grads = torch.empty_like(x), []
+    for t in (gt, F):
+        dw, db = (torch.empty(n, dtype=t, device="cuda") for _ in range(2))
+        zs.zero_layernorm_backward(dy, x, None, mean, rstd, dx, dw=dw, db=db)
+        zs.zero_layernorm_backward(dy, x, None, mean, rstd, dx, db=torch.empty_like(db))
+        grads.append((dw, db))
+    for a, b in zip(*grads):
+        assert torch.equal(a, b.to(gt))  # one sum, rounded once

@@ -33,14 +33,14 @@ def _declare(L):
 _declare(_lib)
 
 
-def _weight_type(w, b, like, other):
+def _weight_type(w, b, *others):
     """the 16-bit type of the flat buffer: the weight's, the bias's, or (with
-    neither) that of whichever of the two matrices is not fp32"""
+    neither) that of the first other tensor that is not fp32"""
     for t, what in ((w, "w"), (b, "b")):
         if t is not None:
             return _in_type(t, what)
-    for t in (like, other):
-        if t.dtype in (torch.bfloat16, torch.float16):
+    for t in others:
+        if t is not None and t.dtype in (torch.bfloat16, torch.float16):
             return t.dtype
     return torch.bfloat16
 
@@ -79,7 +79,7 @@ def zero_layernorm_backward(dy, x, w, mean, rstd, dx, residual=None, dw=None, db
     they hold.  A workspace tensor is allocated where one is needed unless one
     of zero_layernorm_workspace_bytes(m, n) bytes is passed."""
     m, n = _shape(x, "x")
-    dt = _weight_type(w, None, x, dy)
+    dt = _weight_type(w, None, x, dy, dw, db)
     xt, yt, dev = _out_type(x, dt, "x"), _out_type(dy, dt, "dy"), x.get_device()
     gt = torch.float32 if dw is None and db is None else \
         _out_type(dw if dw is not None else db, dt, "dw" if dw is not None else "db")
