@@ -788,8 +788,9 @@ zero_status launch_back(BackArgs a, void *stream) {
     Grads how = grads ? SUMS : NONE;
     if (a.m > 0 && in_registers(a.n)) {
         // One piece a lane up to 8192 elements, three or four beyond; two of
-        // 16-bit rows that fill eight waves exactly, where there are many
-        // (4096 wide: 16384 rows 104 us for 119, 8192 60 for 64, 4096 37 for
+        // 16-bit rows that take eight waves, where there are many (16384 rows
+        // of 3592 103 us for 121, of 3840 101 for 121, of 4096 106 for 120;
+        // 8192 of them 59 for 66, 58 for 66, 61 for 65, 4096 of 4096 37 for
         // 36).  One workgroup on a CU keeps the column sums that go through
         // memory few (16384 x 1600 fp32 82 us for two's 88, 4096 x 4500 42 for
         // 47).  Two pay where x is 16-bit, each has rows enough, and one is
@@ -810,8 +811,11 @@ zero_status launch_back(BackArgs a, void *stream) {
         // One launch for two, which read x and dy twice: a row of 1600 7.3 ->
         // 3.0 us, 256 rows 10.7 -> 4.7, 512 10.7 -> 10.1, 1023 11.7 -> 17.8;
         // 256 of 11008 18.9 -> 9.6, 512 of 600 9.7 -> 6.5 (replayed from a
-        // graph).  Not in place: nobody may write dy before the columns'
-        // workgroups have read it.
+        // graph).  Of 13 widths from 64 to 16384 all gain at 256 rows, 11 to
+        // 58 %; at 512 up to 35 %, but 2304 loses (11.5 -> 14.6) and, with x
+        // and dy fp32, 2304 and 6401 do (12.5 -> 15.6, 19.9 -> 22.4); at 768
+        // as many lose as gain.  Not in place: nobody may write dy before the
+        // columns' workgroups have read it.
         if (grads && a.m <= kFewRows && a.dx != a.dy) how = FEW;
         switch (ceil_div(waves, W)) {
             case 1: run_back<T, XF, DF, 1>(a, threads, how, st); break;
