@@ -100,9 +100,9 @@ ZERO_API int64_t zero_orthogonalize_workspace_bytes(int64_t count, int64_t rows,
  * Singular values must stay below 16 in every round (with the default
  * coefficients they stay below 1.3).  Coefficients that could lift a singular
  * value of up to 1 above 4, or whose b s^2 + c s^4 could spread over more than
- * 16, leave the small elements of A or of the polynomial fewer bits.  Inf or NaN in a matrix makes all of that matrix NaN, and
- * no other; a matrix of zeros stays zero where eps > 0 and is NaN where eps
- * is 0.
+ * 16, leave the small elements of A or of the polynomial fewer bits.  Inf or
+ * NaN in a matrix makes all of that matrix NaN, and no other; a matrix of zeros
+ * stays zero where eps > 0 and is NaN where eps is 0.
  * 0 <= count <= 65535, 0 <= rows, cols <= 65536, a stack spans at most 2^60
  * elements, and a call has less than 2^23 tiles (of 64 x 64 to 256 x 256).  A
  * matrix occupies its span, from its first element to one past its last, and
